@@ -25,6 +25,9 @@ __all__ = [
     "quantize_fp8_1x128",
     "m_grouped_gemm_fp8_fp8_bf16_nt_contiguous",
     "m_grouped_gemm_fp8_fp8_bf16_nt_masked",
+    "m_grouped_gemm_nt_ragged",
+    "m_grouped_gemm_nn_ragged",
+    "k_grouped_gemm_tn_ragged",
     "get_m_alignment_for_contiguous_layout",
     "get_tma_aligned_size",
     "get_col_major_tma_aligned_tensor",
@@ -36,6 +39,7 @@ __all__ = [
     "force_config",
     "force_swap_ab",
     "force_tail_split",
+    "force_ragged",
     "status_string",
     "KIND_DENSE",
     "KIND_CONTIGUOUS",
@@ -102,6 +106,10 @@ def load_library():
         lib.dg_force_config.argtypes = [I, I, I, I]
         lib.dg_force_swap_ab.argtypes = [I]
         lib.dg_force_tail_split.argtypes = [I]
+        lib.m_grouped_gemm_nt_ragged.argtypes = [P, P, P, P, I, I, I, I, I, P]
+        lib.m_grouped_gemm_nn_ragged.argtypes = [P, P, P, P, I, I, I, I, I, P]
+        lib.k_grouped_gemm_tn_ragged.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P]
+        lib.dg_force_ragged.argtypes = [I, I, I]
         _lib = lib
         return lib
 
@@ -240,6 +248,93 @@ def m_grouped_gemm_fp8_fp8_bf16_nt_masked(a, sa, b, sb, d, masked_m, expected_m:
     return d
 
 
+_DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_HALF = (torch.bfloat16, torch.float16)
+_I32 = (torch.int32,)
+
+
+def _call(name: str, stream, device: torch.device, *args) -> None:
+    """Call the library on the tensors' own device, on `stream` or that device's current one."""
+    lib = _lib or load_library()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    fn = getattr(lib, name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        raise Fp8NtError(status, name)
+
+
+def _same_device(*tensors: torch.Tensor) -> torch.device:
+    device = tensors[0].device
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    return device
+
+
+def _ragged(name: str, a, b, d, offsets, G: int, N: int, K: int, stream):
+    dtypes = (a.dtype,) if a.dtype in _HALF else _HALF
+    args = (_dev(a, "a", dtypes, 2), _dev(b, "b", dtypes, 3), _dev(d, "d", dtypes, 2),
+            _dev(offsets, "offsets", _I32, 1))
+    _call(name, stream, _same_device(a, b, d, offsets), *args, _DTYPE_CODE[a.dtype], G, a.shape[0],
+          N, K)
+    return d
+
+
+def m_grouped_gemm_nt_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
+                             offsets: torch.Tensor, stream=None) -> torch.Tensor:
+    """Grouped product over ragged segments: d[t] = a[t] b[g]^T for rows t of segment g.
+
+    a: [T,K] bf16 or fp16; b: [G,N,K], d: [T,N] of the same type; offsets: [G+1]
+    int32 on the device, segment g being rows offsets[g] to offsets[g+1] (any
+    length, no padding).  Rows outside every segment are left as they are.
+    """
+    G, N, K = b.shape
+    if a.shape[1] != K or tuple(d.shape) != (a.shape[0], N) or offsets.shape[0] != G + 1:
+        raise ValueError("shape mismatch between a, b, d and offsets")
+    return _ragged("m_grouped_gemm_nt_ragged", a, b, d, offsets, G, N, K, stream)
+
+
+def m_grouped_gemm_nn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
+                             offsets: torch.Tensor, stream=None) -> torch.Tensor:
+    """Input gradient of m_grouped_gemm_nt_ragged: d[t] = a[t] b[g] for rows t of segment g.
+
+    a: [T,N] (gradients of the forward's output); b: [G,N,K] (the forward's
+    weights, not transposed); d: [T,K]; offsets as in the forward.
+    """
+    G, N, K = b.shape
+    if a.shape[1] != N or tuple(d.shape) != (a.shape[0], K) or offsets.shape[0] != G + 1:
+        raise ValueError("shape mismatch between a, b, d and offsets")
+    return _ragged("m_grouped_gemm_nn_ragged", a, b, d, offsets, G, N, K, stream)
+
+
+def k_grouped_gemm_tn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
+                             offsets: torch.Tensor, accumulate: bool = False,
+                             stream=None) -> torch.Tensor:
+    """Weight gradient of m_grouped_gemm_nt_ragged: d[g] = a[segment g]^T b[segment g].
+
+    a: [T,N] (gradients of the forward's output); b: [T,K] (the forward's
+    input), both bf16 or fp16; d: [G,N,K] fp32 or their type.  accumulate: add to
+    d (fp32 only), else d is written in full (zeros for a group without rows).
+    """
+    G, N, K = d.shape
+    if a.shape[1] != N or b.shape[1] != K or a.shape[0] != b.shape[0] or offsets.shape[0] != G + 1:
+        raise ValueError("shape mismatch between a, b, d and offsets")
+    dtypes = (a.dtype,) if a.dtype in _HALF else _HALF
+    args = (_dev(a, "a", dtypes, 2), _dev(b, "b", dtypes, 2),
+            _dev(d, "d", dtypes if not accumulate else _F32, 3) if d.dtype != torch.float32
+            else _dev(d, "d", _F32, 3), _dev(offsets, "offsets", _I32, 1))
+    _call("k_grouped_gemm_tn_ragged", stream, _same_device(a, b, d, offsets), *args,
+          _DTYPE_CODE[a.dtype], _DTYPE_CODE[d.dtype], int(accumulate), G, a.shape[0], N, K)
+    return d
+
+
 def get_m_alignment_for_contiguous_layout() -> int:
     return load_library().get_m_alignment_for_contiguous_layout()
 
@@ -313,3 +408,10 @@ def force_tail_split(mode: int = 0) -> None:
     0 = automatic (off), 1 = never, 2 = wherever the block layout allows it,
     3 = where the layout allows it and the cycle estimate favours it."""
     _check(load_library().dg_force_tail_split(int(mode)), "dg_force_tail_split")
+
+
+def force_ragged(swap_ab: int = 0, cta_pair: int = 0, block_n: int = 0) -> None:
+    """Pin the tile form of later ragged grouped calls (0, 0, 0 = automatic):
+    swap_ab 1 = weights on the 128-row side and block_n token rows; cta_pair 1 =
+    256 x 256 by CTA pairs; block_n alone = 128 x block_n.  For tests."""
+    _check(load_library().dg_force_ragged(int(swap_ab), int(cta_pair), int(block_n)), "dg_force_ragged")

@@ -3,7 +3,8 @@
 Compiles csrc/api.cu and one object per kernel shape listed in
 csrc/kernels.def (csrc/instance.cu with -DFP8NT_MW / -DFP8NT_BN / -DFP8NT_PAIR / -DFP8NT_SCALAR)
 and per small-M kernel listed in csrc/skinny.def (csrc/instance_skinny.cu with
--DFP8NT_SKINNY_MN), in parallel, then links them with the static CUDA runtime.  ptxas's resource
+-DFP8NT_SKINNY_MN) and per ragged grouped kernel listed in csrc/ragged.def
+(csrc/instance_ragged.cu with -DFP8NT_R_*), in parallel, then links them with the static CUDA runtime.  ptxas's resource
 report is checked for every kernel: the kernels rebalance registers between
 warpgroups with setmaxnreg, which is only safe when each kernel is launched
 with exactly the per-thread register count that split assumes, and spills are
@@ -64,6 +65,18 @@ def skinny_list() -> list[int]:
             if m:
                 mns.append(int(m.group(1)))
     return mns
+
+
+def ragged_list() -> list[tuple[int, int, int, int]]:
+    """(DIR, SWAP, PAIR, BN) of every ragged grouped kernel listed in csrc/ragged.def."""
+    shapes = []
+    with open(os.path.join(CSRC, "ragged.def")) as f:
+        for line in f:
+            m = re.match(r"\s*FP8NT_RAGGED\(\s*(\d+)\s*,\s*(\d+)\s*,\s*(\d+)\s*,\s*(\d+)\s*\)",
+                         line)
+            if m:
+                shapes.append(tuple(int(m.group(i)) for i in range(1, 5)))
+    return shapes
 
 
 def kernel_shapes() -> list[tuple[int, int, int]]:
@@ -130,11 +143,8 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
             and open(stamp).read() == digest):
         return LIB_PATH
     jobs = jobs or max(1, os.cpu_count() or 1)
-    tasks = [(os.path.join(CSRC, "api.cu"), os.path.join(BUILD_DIR, "api.o"), [], "api"),
-             (os.path.join(CSRC, "quantize.cu"), os.path.join(BUILD_DIR, "quantize.o"), [],
-              "quantize"),
-             (os.path.join(CSRC, "selftest.cu"), os.path.join(BUILD_DIR, "selftest.o"), [],
-              "selftest")]
+    tasks = [(os.path.join(CSRC, f"{name}.cu"), os.path.join(BUILD_DIR, f"{name}.o"), [], name)
+             for name in ("api", "api_grouped", "quantize", "selftest")]
     for mw, bn, pair, scalar in kernel_list():
         tag = f"mw{mw}_bn{bn}_p{pair}_s{scalar}"
         tasks.append((os.path.join(CSRC, "instance.cu"), os.path.join(BUILD_DIR, f"kernel_{tag}.o"),
@@ -144,6 +154,11 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         tasks.append((os.path.join(CSRC, "instance_skinny.cu"),
                       os.path.join(BUILD_DIR, f"skinny_mn{mn}.o"), [f"-DFP8NT_SKINNY_MN={mn}"],
                       f"skinny_mn{mn}"))
+    for d, swap, pair, bn in ragged_list():
+        tag = f"ragged_d{d}_s{swap}_p{pair}_bn{bn}"
+        tasks.append((os.path.join(CSRC, "instance_ragged.cu"), os.path.join(BUILD_DIR, f"{tag}.o"),
+                      [f"-DFP8NT_R_DIR={d}", f"-DFP8NT_R_SWAP={swap}", f"-DFP8NT_R_PAIR={pair}",
+                       f"-DFP8NT_R_BN={bn}"], tag))
     notes = []
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         futures = [(t, pool.submit(_compile, t[0], t[1], t[2])) for t in tasks]

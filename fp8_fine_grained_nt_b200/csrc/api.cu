@@ -11,6 +11,7 @@
 #include <string.h>
 
 #include "fp8_nt.h"
+#include "grouped.h"
 #include "launch.h"
 #include "params.h"
 
@@ -900,6 +901,47 @@ int run(const Problem &pb, const void *A, const float *sa, const void *B, const 
 }
 
 } // namespace
+
+// ------------------------------------------------------------------ shared with the row-grouped operators
+
+namespace fp8nt {
+
+int current_device(DeviceView *out)
+{
+    DeviceInfo *dev = nullptr;
+    const int st = device_info(&dev);
+    if (st != DG_OK)
+        return st;
+    out->index = (int)(dev - g_devices);
+    out->sms = effective_sms(dev);
+    out->max_smem = dev->max_smem;
+    out->status = dev->status;
+    out->timeout_ns = wait_timeout_ns();
+    return DG_OK;
+}
+
+int make_tmap_128b(CUtensorMap *map, const void *base, CUtensorMapDataType type, int rank, const uint64_t *dims,
+                   const uint64_t *strides, const uint32_t *box)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return DG_ERR_CUDA;
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], e[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank)
+            st[i] = strides[i];
+    }
+    return fn(map, type, (cuuint32_t)rank, const_cast<void *>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? DG_OK
+               : DG_ERR_CUDA;
+}
+
+} // namespace fp8nt
 
 // ====================================================================== C ABI
 

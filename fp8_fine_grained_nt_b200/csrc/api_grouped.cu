@@ -1,0 +1,266 @@
+// C-ABI entry points of the row-grouped operators (declared in
+// include/fp8_nt.h): argument validation, kernel choice, tensor maps, launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <stdint.h>
+#include <string.h>
+
+#include "fp8_nt.h"
+#include "grouped.h"
+
+using namespace fp8nt;
+
+namespace {
+
+struct RaggedKernel {
+    int dir, swap, pair, bn;
+    RaggedLaunchFn launch;
+};
+
+const RaggedKernel kRagged[] = {
+#define FP8NT_RAGGED(d, s, p, n) {d, s, p, n, launch_ragged_d##d##_s##s##_p##p##_bn##n},
+#include "ragged.def"
+#undef FP8NT_RAGGED
+};
+constexpr int kNumRagged = sizeof(kRagged) / sizeof(kRagged[0]);
+
+// test hook: swap (0 / 1), pair (0 / 1) and bn of later calls, 0 = automatic
+std::atomic<uint32_t> g_forced_ragged{0};
+
+bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+// The kernel of a call.
+const RaggedKernel *choose_ragged(int dir, int groups, int rows, int N, int K)
+{
+    const uint32_t forced = g_forced_ragged.load(std::memory_order_relaxed);
+    if (forced) {
+        for (int i = 0; i < kNumRagged; ++i) {
+            const RaggedKernel &k = kRagged[i];
+            if (k.dir == dir && ((uint32_t)k.bn | (uint32_t)k.swap << 16 | (uint32_t)k.pair << 17) == forced)
+                return &k;
+        }
+    }
+    int swap = 0, pair = 1, bn = 256;
+    if (dir == RAGGED_TN) {
+        if (N <= 128 || K <= 128) {
+            pair = 0;
+            bn = 128;
+        }
+    } else {
+        const long mean = ceil_div(rows, groups);
+        if (mean <= 128) {
+            swap = 1;
+            pair = 0;
+            bn = mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+        }
+    }
+    for (int i = 0; i < kNumRagged; ++i)
+        if (kRagged[i].dir == dir && kRagged[i].swap == swap && kRagged[i].pair == pair && kRagged[i].bn == bn)
+            return &kRagged[i];
+    return nullptr;
+}
+
+int check_ragged(int dir, const void *A, const void *B, void *D, const int *offsets, int dtype, int G, int M_sum,
+                 int N, int K)
+{
+    if (G <= 0 || M_sum < 0 || N < 0 || K < 0 || (dtype != DG_INPUT_BF16 && dtype != DG_INPUT_F16))
+        return DG_ERR_INVALID_ARGUMENT;
+    if (G > RAGGED_MAX_GROUPS || N == 0 || K == 0 || N % 8 != 0 || K % 8 != 0)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    // bytes of one group's weights: the stride of a tensor map's group axis
+    if ((uint64_t)N * (uint64_t)K * 4u >= (1ull << 40))
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    // tiles of the smallest tile form are counted in 32 bits
+    if ((ceil_div(M_sum, 32) + G) * ceil_div(N > K ? N : K, 128) > 0x7fffffffL ||
+        (long)G * ceil_div(N, 128) * ceil_div(K, 128) > 0x7fffffffL)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    // without rows only the weight gradient has anything to write
+    if (M_sum == 0 && dir != RAGGED_TN)
+        return DG_OK;
+    if (!D || !offsets || (M_sum > 0 && (!A || !B)))
+        return DG_ERR_INVALID_ARGUMENT;
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || !aligned(offsets, 4))
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+int run_ragged(int dir, const void *A, const void *B, void *D, const int *offsets, int dtype, int d_type,
+               int accumulate, int G, int M_sum, int N, int K, cudaStream_t stream)
+{
+    DeviceView dev;
+    int st = current_device(&dev);
+    if (st != DG_OK)
+        return st;
+    const bool tn = dir == RAGGED_TN;
+    if (M_sum == 0) {
+        if (!tn || accumulate)
+            return DG_OK;
+        const size_t bytes = (size_t)G * N * K * (d_type == RAGGED_OUT_F32 ? 4 : 2);
+        return cudaMemsetAsync(D, 0, bytes, stream) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+    }
+    const RaggedKernel *k = choose_ragged(dir, G, M_sum, N, K);
+    if (!k)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    const bool bf16 = dtype == DG_INPUT_BF16;
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const int bm = k->pair ? 256 : 128;
+    const uint32_t y_rows = (uint32_t)(k->pair ? k->bn / 2 : k->bn);
+
+    RaggedParams p;
+    memset(&p, 0, sizeof(p));
+    p.offsets = offsets;
+    p.d = D;
+    p.status = dev.status;
+    p.timeout_ns = dev.timeout_ns;
+    p.num_groups = G;
+    p.total_rows = M_sum;
+    p.out_type = d_type;
+    p.accumulate = accumulate;
+    const int out = dir == RAGGED_NT ? N : K; // columns of the result
+    const int red = dir == RAGGED_NT ? K : N; // reduction of NT, NN
+    p.d_rows = N;
+    p.d_cols = out;
+    p.nkb = (int)ceil_div(red, RAGGED_BK);
+    long tiles;
+    if (tn) {
+        p.x_blocks = (int)ceil_div(N, bm);
+        p.y_blocks = (int)ceil_div(K, k->bn);
+        p.tiles_per_group = p.x_blocks * p.y_blocks;
+        tiles = (long)G * p.tiles_per_group;
+    } else {
+        p.x_blocks = (int)ceil_div(out, 128);
+        p.y_blocks = (int)ceil_div(out, k->bn);
+        const long tok_blocks = M_sum / (k->swap ? k->bn : bm) + (G < M_sum ? G : M_sum);
+        tiles = tok_blocks * (k->swap ? p.x_blocks : p.y_blocks);
+    }
+    const bool x_mn = tn || (dir == RAGGED_NN && k->swap);
+    const bool y_mn = tn || (dir == RAGGED_NN && !k->swap);
+    p.idesc = ragged_idesc(bf16, x_mn, y_mn, bm, k->bn);
+
+    // shared memory: the deepest operand ring beside the output staging
+    const uint32_t stage = 128u * 128u + y_rows * 128u;
+    const int slots = k->swap ? 0 : k->pair && !tn ? 1 : 2;
+    int stages = RAGGED_MAX_STAGES;
+    for (; stages >= 2; --stages) {
+        make_ragged_plan(p, stage, stages, slots);
+        if ((int)p.total + 1024 <= dev.max_smem)
+            break;
+    }
+    if (stages < 2)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+
+    // operand boxes: 64 reduction elements of all rows (K-major), or 64 rows
+    // of the reduction x 64 elements (MN-major); tokens [M_sum][cols], weights
+    // [G][N][K]
+    auto tokens = [&](CUtensorMap *map, const void *base, int cols, bool mn, uint32_t rows) {
+        const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)M_sum}, strides[1] = {(uint64_t)cols * 2};
+        const uint32_t box[2] = {64, mn ? 64u : rows};
+        return make_tmap_128b(map, base, type, 2, dims, strides, box);
+    };
+    auto weights = [&](CUtensorMap *map, const void *base, bool mn, uint32_t rows) {
+        const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)G};
+        const uint64_t strides[2] = {(uint64_t)K * 2, (uint64_t)N * (uint64_t)K * 2};
+        const uint32_t box[3] = {64, mn ? 64u : rows, 1};
+        return make_tmap_128b(map, base, type, 3, dims, strides, box);
+    };
+    CUtensorMap tx, ty, td;
+    memset(&td, 0, sizeof(td));
+    if (tn) {
+        st = tokens(&tx, A, N, true, 0);
+        if (st == DG_OK)
+            st = tokens(&ty, B, K, true, 0);
+        if (st == DG_OK) {
+            const uint64_t size = d_type == RAGGED_OUT_F32 ? 4 : 2;
+            const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)G};
+            const uint64_t strides[2] = {(uint64_t)K * size, (uint64_t)N * (uint64_t)K * size};
+            const uint32_t box[3] = {(uint32_t)(128 / size), 32, 1};
+            st = make_tmap_128b(&td, D, d_type == RAGGED_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                        : d_type == RAGGED_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                3, dims, strides, box);
+        }
+    } else {
+        CUtensorMap *tok = k->swap ? &ty : &tx, *wgt = k->swap ? &tx : &ty;
+        st = tokens(tok, A, red, false, k->swap ? y_rows : 128u);
+        if (st == DG_OK)
+            st = weights(wgt, B, dir == RAGGED_NN, k->swap ? 128u : y_rows);
+        if (st == DG_OK && !k->swap) {
+            const uint64_t dims[2] = {(uint64_t)out, (uint64_t)M_sum}, strides[1] = {(uint64_t)out * 2};
+            const uint32_t box[2] = {64, 32};
+            st = make_tmap_128b(&td, D, type, 2, dims, strides, box);
+        }
+    }
+    if (st != DG_OK)
+        return st;
+    RaggedLaunchArgs args;
+    args.tmap_x = &tx;
+    args.tmap_y = &ty;
+    args.tmap_d = &td;
+    args.params = &p;
+    args.device = dev.index;
+    args.max_smem = dev.max_smem;
+    const long ctas = k->pair ? 2 * tiles : tiles;
+    const int sms = k->pair ? (dev.sms > 1 ? dev.sms / 2 * 2 : 2) : dev.sms;
+    args.grid = (int)(ctas < sms ? ctas : sms);
+    args.smem_bytes = (int)p.total + 1024;
+    args.stream = stream;
+    return k->launch(args) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+} // namespace
+
+// ====================================================================== C ABI
+
+extern "C" {
+
+int m_grouped_gemm_nt_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype, int num_groups,
+                             int M_sum, int N, int K, dg_stream_t stream)
+{
+    const int st = check_ragged(RAGGED_NT, A, B, D, offsets, dtype, num_groups, M_sum, N, K);
+    return st != DG_OK ? st
+                       : run_ragged(RAGGED_NT, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
+                                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+int m_grouped_gemm_nn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype, int num_groups,
+                             int M_sum, int N, int K, dg_stream_t stream)
+{
+    const int st = check_ragged(RAGGED_NN, A, B, D, offsets, dtype, num_groups, M_sum, N, K);
+    return st != DG_OK ? st
+                       : run_ragged(RAGGED_NN, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
+                                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype, int d_dtype,
+                             int accumulate, int num_groups, int M_sum, int N, int K, dg_stream_t stream)
+{
+    const int st = check_ragged(RAGGED_TN, A, B, D, offsets, dtype, num_groups, M_sum, N, K);
+    if (st != DG_OK)
+        return st;
+    // the result is FP32 or the operands' type; adding to it needs FP32, so
+    // that a sum over many calls is not rounded to 16 bits at each
+    if ((d_dtype != DG_INPUT_F32 && d_dtype != dtype) || (accumulate && d_dtype != DG_INPUT_F32))
+        return DG_ERR_INVALID_ARGUMENT;
+    return run_ragged(RAGGED_TN, A, B, D, offsets, dtype, d_dtype, accumulate != 0, num_groups, M_sum, N, K,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dg_force_ragged(int swap_ab, int cta_pair, int block_n)
+{
+    if (swap_ab == 0 && cta_pair == 0 && block_n == 0) {
+        g_forced_ragged.store(0, std::memory_order_relaxed);
+        return DG_OK;
+    }
+    for (int i = 0; i < kNumRagged; ++i)
+        if (kRagged[i].swap == swap_ab && kRagged[i].pair == cta_pair && kRagged[i].bn == block_n) {
+            g_forced_ragged.store((uint32_t)block_n | (uint32_t)swap_ab << 16 | (uint32_t)cta_pair << 17,
+                                  std::memory_order_relaxed);
+            return DG_OK;
+        }
+    return DG_ERR_UNSUPPORTED_SHAPE;
+}
+
+} // extern "C"

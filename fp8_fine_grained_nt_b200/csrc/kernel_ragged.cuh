@@ -1,0 +1,611 @@
+// Persistent tcgen05 kernel for 16-bit (BF16 or FP16) matrix products grouped
+// by expert over row segments of any length, in the three directions of a
+// grouped linear layer.  Segment g is rows [offsets[g], offsets[g + 1]).
+//
+//   NT (forward)          d[t, n]    = sum_k a[t, k] b[g, n, k]
+//   NN (input gradient)   d[t, k]    = sum_n a[t, n] b[g, n, k]
+//   TN (weight gradient)  d[g, n, k] = sum_{t in g} a[t, n] b[t, k]
+//
+// All three are P[i, j] = sum_r X[i, r] Y[j, r] over 64-wide blocks of r, and
+// the tensor core reads an operand either with r contiguous ("K-major") or
+// with i / j contiguous ("MN-major"), so no operand is ever transposed in
+// memory: NT reads both K-major, NN reads b MN-major, TN reads both MN-major.
+// Accumulation is FP32 in tensor memory over the whole reduction; the result
+// is rounded once, on store.
+//
+// Tile forms:
+//   PAIR   256 x 256 by a cluster of two CTAs (cta_group::2): each CTA loads
+//          its own 128 rows of X and half of Y, so per CTA a 64-wide block
+//          brings 32 KB for 512 cycles of MMA.  For many rows per group and
+//          for weight gradients.
+//   single 128 x BN by one CTA.
+//   SWAP   the weights are X (128 of the output's columns per tile) and BN
+//          token rows are Y: for few rows per group, where the call is bound
+//          by reading the weights and 128 token rows would be mostly padding.
+//
+// Roles (256 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
+// allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
+// only), warps 4-7 epilogue (one 32-lane quarter of tensor memory each).  Two
+// accumulators in tensor memory let a tile's epilogue overlap the next
+// tile's MMAs.
+#pragma once
+
+#include "kernel.cuh"
+#include "ragged_params.h"
+
+namespace fp8nt {
+
+template <int DIR, bool SWAP, bool PAIR, int BN>
+struct RaggedTraits {
+    static_assert(!PAIR || (BN == 256 && !SWAP), "a CTA pair computes 256 x 256");
+    static_assert(DIR != RAGGED_TN || !SWAP, "the weight gradient has no swapped form");
+    static constexpr int BM = PAIR ? 256 : 128;      // rows of X per tile
+    static constexpr int Y_ROWS = PAIR ? BN / 2 : BN; // rows of Y each CTA loads
+    // a side is MN-major where its i / j index is the contiguous one in memory
+    static constexpr bool X_MN = DIR == RAGGED_TN || (DIR == RAGGED_NN && SWAP);
+    static constexpr bool Y_MN = DIR == RAGGED_TN || (DIR == RAGGED_NN && !SWAP);
+    static_assert(!Y_MN || Y_ROWS % 64 == 0, "MN-major operands load in 64-wide chunks");
+    static constexpr uint32_t X_BYTES = 128 * 128;
+    static constexpr uint32_t Y_BYTES = Y_ROWS * 128;
+    static constexpr uint32_t STAGE_BYTES = X_BYTES + Y_BYTES;
+    static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "power of two, at most 512");
+};
+
+struct RaggedTile {
+    int g;
+    int first; // first row of the group's segment
+    int rows;  // rows of the segment
+    int i0;    // tile's first X row: token (relative to the segment) or output index
+    int j0;    // tile's first Y row
+    int nkb;   // 64-wide blocks of the reduction
+};
+
+// Tile t.  `tiles` holds the tile prefix sums of the groups (NT, NN); order
+// within a group: bands of 8 X blocks, X fastest within a band, so that the
+// tiles in flight share both operands in L2.  SWAP: the token blocks of one
+// weight block run side by side.
+template <int DIR, bool SWAP, int BM, int BN>
+__device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, const int *tiles, const int *first,
+                                                  const int *count)
+{
+    RaggedTile r;
+    int local, xb, yb;
+    if (DIR == RAGGED_TN) {
+        r.g = t / p.tiles_per_group;
+        local = t - r.g * p.tiles_per_group;
+        xb = p.x_blocks;
+        yb = p.y_blocks;
+    } else {
+        int lo = 0, hi = p.num_groups - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tiles[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        r.g = lo;
+        local = t - tiles[lo];
+        const int tok_blocks = (count[lo] + (SWAP ? BN : BM) - 1) / (SWAP ? BN : BM);
+        xb = SWAP ? p.x_blocks : tok_blocks;
+        yb = SWAP ? tok_blocks : p.y_blocks;
+    }
+    r.first = first[r.g];
+    r.rows = count[r.g];
+    if (SWAP) {
+        r.i0 = local / yb * BM;
+        r.j0 = local % yb * BN;
+    } else {
+        const int band = local / (8 * yb);
+        const int in_band = local - band * 8 * yb;
+        const int width = min(8, xb - band * 8);
+        r.i0 = (band * 8 + in_band % width) * BM;
+        r.j0 = in_band / width * BN;
+    }
+    r.nkb = DIR == RAGGED_TN ? (r.rows + RAGGED_BK - 1) / RAGGED_BK : p.nkb;
+    return r;
+}
+
+__device__ __forceinline__ bool wait_ragged(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                            const RaggedParams &p)
+{
+    const uint32_t a = smem_addr(bar);
+    return mbar_try_wait(a, parity) || wait_slow(a, parity, abort_flag, p.status, p.timeout_ns, true);
+}
+
+__device__ __forceinline__ void drain_ragged(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                             const RaggedParams &p)
+{
+    const uint32_t a = smem_addr(bar);
+    if (!mbar_try_wait(a, parity))
+        wait_slow(a, parity, abort_flag, p.status, p.timeout_ns, false);
+}
+
+// One operand's 64-wide reduction block: K-major, one box of ROWS rows of 128
+// bytes; MN-major, ROWS / 64 boxes of 64 reduction rows of 128 bytes.
+// GROUPED: the tensor has a group axis.  LEADER: completion is counted on the
+// pair leader's barrier at cluster address `bar`.
+template <bool MN, bool GROUPED, bool LEADER, int ROWS>
+__device__ __forceinline__ void ragged_load(uint8_t *dst, const CUtensorMap *map, uint32_t bar, int mn, int red, int g)
+{
+#pragma unroll
+    for (int c = 0; c < (MN ? ROWS / 64 : 1); ++c) {
+        const int x = MN ? mn + 64 * c : red;
+        const int y = MN ? red : mn;
+        tma_load_nd<GROUPED, LEADER>(dst + c * 8192, map, bar, x, y, g);
+    }
+}
+
+// Shared-memory descriptor of an operand at `saddr`: K-major as make_sdesc;
+// MN-major, 64 elements (128 bytes, swizzled) along i / j, 8-row groups of the
+// reduction 1024 bytes apart, the next 64 elements 8192 bytes on.
+template <bool MN>
+__device__ __forceinline__ uint64_t ragged_desc(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(MN ? 8192u >> 4 : 1u) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// Two FP32 values rounded to nearest even in the result's 16-bit type.
+__device__ __forceinline__ uint32_t pack_16x2(float lo, float hi, bool bf16)
+{
+    if (bf16)
+        return pack_bf16x2(lo, hi);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int DIR, bool SWAP, bool PAIR, int BN>
+__global__ void __launch_bounds__(RAGGED_THREADS, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_y,
+                  const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ RaggedParams p)
+{
+    using T = RaggedTraits<DIR, SWAP, PAIR, BN>;
+    constexpr bool TN = DIR == RAGGED_TN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stages = (uint32_t)p.stages;
+
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + p.off_bars); // stage holds its operands
+    uint64_t *empty = full + RAGGED_MAX_STAGES;                       // its MMAs have completed
+    uint64_t *tail_full = empty + RAGGED_MAX_STAGES;                  // TN: a segment's last block landed here
+    uint64_t *tail_ready = tail_full + RAGGED_MAX_STAGES;             // and its foreign rows are cleared
+    uint64_t *acc_full = tail_ready + RAGGED_MAX_STAGES;              // accumulator complete (x2)
+    uint64_t *acc_empty = acc_full + 2;                               // accumulator read (x2)
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + p.off_misc);
+    volatile uint32_t *abort_flag = misc + 1;
+    int *tiles = reinterpret_cast<int *>(smem + p.off_groups);
+    int *first = tiles + p.num_groups + 1;
+    int *count = first + p.num_groups;
+
+    // ---------------------------------------------------------------- set-up
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&tail_full[s], 1);
+            mbar_init(&tail_ready[s], PAIR ? 2 : 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], PAIR ? 8 : 4);
+        }
+        mbar_init(mma_done, 1);
+        misc[1] = 0u;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmap_x);
+        tma_prefetch_desc(&tmap_y);
+        tma_prefetch_desc(&tmap_d);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(misc, T::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(misc, T::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    // the previous kernel's results are visible from here on; a next one may
+    // set itself up
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // Segments, clamped into [0, total]; a bad offset is flagged.  Each
+    // thread takes `per` consecutive groups; exclusive prefix sums of their
+    // tiles by a block scan.
+    {
+        const int per = (p.num_groups + RAGGED_THREADS - 1) / RAGGED_THREADS;
+        const int g0 = threadIdx.x * per;
+        int mine = 0;
+        bool bad = false;
+        for (int g = g0; g < min(g0 + per, p.num_groups); ++g) {
+            const int lo = __ldg(p.offsets + g), hi = __ldg(p.offsets + g + 1);
+            const int a = min(max(lo, 0), p.total_rows);
+            const int b = min(max(hi, a), p.total_rows);
+            bad |= lo != a || hi != b;
+            first[g] = a;
+            count[g] = b - a;
+            if (!TN) {
+                constexpr int TOK = SWAP ? BN : T::BM;
+                mine += (b - a + TOK - 1) / TOK * (SWAP ? p.x_blocks : p.y_blocks);
+            }
+        }
+        if (bad)
+            atomicOr(p.status, DEVERR_BAD_INDEX);
+        if (!TN) {
+            int incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d)
+                    incl += v;
+            }
+            if (lane == 31)
+                misc[4 + warp] = (uint32_t)incl;
+            __syncthreads();
+            int at = incl - mine;
+            for (int w = 0; w < warp; ++w)
+                at += (int)misc[4 + w];
+            for (int g = g0; g < min(g0 + per, p.num_groups); ++g) {
+                constexpr int TOK = SWAP ? BN : T::BM;
+                tiles[g] = at;
+                at += (count[g] + TOK - 1) / TOK * (SWAP ? p.x_blocks : p.y_blocks);
+            }
+            if (threadIdx.x == RAGGED_THREADS - 1)
+                tiles[p.num_groups] = at;
+        }
+    }
+    tc_fence_before();
+    if constexpr (PAIR)
+        cluster_sync(); // the peer may arrive on the leader's barriers from here on
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = misc[0];
+    const int num_tiles = TN ? p.num_groups * p.tiles_per_group : tiles[p.num_groups];
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int t_first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
+    const int t_stride = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            uint32_t it = 0, s = 0, phase = 1;
+            uint32_t plain = 0; // per stage: its last use was counted on full[]
+            bool ok = true;
+            for (int t = t_first; ok && t < num_tiles; t += t_stride) {
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+                const int x_mn = ti.i0 + (PAIR ? (int)rank * 128 : 0) + ((!TN && !SWAP) ? ti.first : 0);
+                const int y_mn = ti.j0 + (PAIR ? (int)rank * T::Y_ROWS : 0) + (SWAP ? ti.first : 0);
+                const int red0 = TN ? ti.first : 0;
+                for (int kb = 0; kb < ti.nkb; ++kb) {
+                    if (!wait_ragged(&empty[s], phase, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = smem + s * T::STAGE_BYTES;
+                    const int red = red0 + kb * RAGGED_BK;
+                    const bool tail = TN && ti.rows - kb * RAGGED_BK < RAGGED_BK;
+                    if (tail) {
+                        // counted by each CTA for itself: warp 2 clears the
+                        // rows of other segments before the MMAs read them
+                        if (leader)
+                            mbar_arrive(&full[s]);
+                        mbar_arrive_expect_tx(&tail_full[s], T::STAGE_BYTES);
+                        const uint32_t bar = smem_addr(&tail_full[s]);
+                        ragged_load<T::X_MN, false, false, 128>(dst, &tmap_x, bar, x_mn, red, ti.g);
+                        ragged_load<T::Y_MN, false, false, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn, red, ti.g);
+                        plain &= ~(1u << s);
+                    } else {
+                        if (leader)
+                            mbar_arrive_expect_tx(&full[s], PAIR ? 2 * T::STAGE_BYTES : T::STAGE_BYTES);
+                        const uint32_t bar =
+                            PAIR ? map_shared_rank(smem_addr(&full[s]), 0u) : smem_addr(&full[s]);
+                        ragged_load<T::X_MN, SWAP, PAIR, 128>(dst, &tmap_x, bar, x_mn, red, ti.g);
+                        ragged_load<T::Y_MN, !TN && !SWAP, PAIR, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn, red,
+                                                                           ti.g);
+                        plain |= 1u << s;
+                    }
+                    ++it;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every copy issued lands before the CTA exits (a peer's copies
+            // are counted on the leader's barriers; warp 2 waits for tails)
+            if (leader) {
+                const uint32_t n = it < stages ? it : stages;
+                for (uint32_t i = it - n; i < it; ++i)
+                    if ((plain >> (i % stages)) & 1u)
+                        drain_ragged(&full[i % stages], (i / stages) & 1, abort_flag, p);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && leader) {
+            const uint32_t base = smem_addr(smem);
+            const uint64_t x0 = ragged_desc<T::X_MN>(base);
+            const uint64_t y0 = ragged_desc<T::Y_MN>(base + T::X_BYTES);
+            constexpr uint32_t X_STEP = (T::X_MN ? 2048u : 32u) >> 4; // 16 along the reduction
+            constexpr uint32_t Y_STEP = (T::Y_MN ? 2048u : 32u) >> 4;
+            uint32_t s = 0, phase = 0, tile_it = 0, tail_phase = 0;
+            bool ok = true;
+            for (int t = t_first; ok && t < num_tiles; t += t_stride) {
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+                if (ti.nkb == 0)
+                    continue;
+                const uint32_t buf = tile_it & 1;
+                if (!wait_ragged(&acc_empty[buf], ((tile_it >> 1) & 1) ^ 1, abort_flag, p))
+                    break;
+                const uint32_t d = tmem_base + buf * (uint32_t)BN;
+                for (int kb = 0; kb < ti.nkb; ++kb) {
+                    if (!wait_ragged(&full[s], phase, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    int steps = RAGGED_BK / 16;
+                    if (TN && ti.rows - kb * RAGGED_BK < RAGGED_BK) {
+                        if (!wait_ragged(&tail_ready[s], (tail_phase >> s) & 1, abort_flag, p)) {
+                            ok = false;
+                            break;
+                        }
+                        tail_phase ^= 1u << s;
+                        steps = (ti.rows - kb * RAGGED_BK + 15) / 16;
+                    }
+                    tc_fence_after();
+                    const uint64_t xd = x0 + s * (T::STAGE_BYTES >> 4);
+                    const uint64_t yd = y0 + s * (T::STAGE_BYTES >> 4);
+#pragma unroll
+                    for (int k = 0; k < RAGGED_BK / 16; ++k)
+                        if (!TN || k < steps)
+                            mma_f16<PAIR>(d, xd + k * X_STEP, yd + k * Y_STEP, p.idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    if constexpr (PAIR)
+                        mma_commit_pair_mc(&empty[s], 0x3);
+                    else
+                        mma_commit(&empty[s]);
+                    if (kb == ti.nkb - 1) {
+                        if constexpr (PAIR)
+                            mma_commit_pair_mc(&acc_full[buf], 0x3);
+                        else
+                            mma_commit(&acc_full[buf]);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                ++tile_it;
+            }
+            // all MMAs complete before tensor memory is released
+            if constexpr (PAIR)
+                mma_commit_pair(mma_done);
+            else
+                mma_commit(mma_done);
+            drain_ragged(mma_done, 0, abort_flag, p);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ segment ends (TN)
+        // The last block of a segment holds rows of the next one (or behind
+        // the last): they are cleared in both operands, so that they count as
+        // zero whatever they hold.  A reduction row is one 128-byte line per
+        // 64-element chunk, wherever the swizzle puts its pieces.
+        if constexpr (TN) {
+            uint32_t s = 0, tail_phase = 0;
+            bool ok = true;
+            for (int t = t_first; ok && t < num_tiles; t += t_stride) {
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+                s = (s + (uint32_t)ti.nkb) % stages;
+                const int valid = ti.rows & (RAGGED_BK - 1);
+                if (valid == 0)
+                    continue;
+                const uint32_t st = (s + stages - 1) % stages; // the segment's last block
+                bool got = wait_ragged(&tail_full[st], (tail_phase >> st) & 1, abort_flag, p);
+                if (!got) // aborting: an issued copy still lands before the CTA exits
+                    drain_ragged(&tail_full[st], (tail_phase >> st) & 1, abort_flag, p);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tail_phase ^= 1u << st;
+                constexpr int CHUNKS = (int)(T::STAGE_BYTES / 8192);
+                const int clear = ((valid + 15) & ~15) - valid;
+                const uint32_t base = smem_addr(smem) + st * T::STAGE_BYTES;
+                for (int i = lane; i < CHUNKS * clear * 8; i += 32) {
+                    const int piece = i & 7, line = i >> 3;
+                    const int c = line / clear, r = valid + line % clear;
+                    st_shared_v4(base + c * 8192 + r * 128 + piece * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        mbar_arrive_cluster_release(map_shared_rank(smem_addr(&tail_ready[st]), 0u));
+                    else
+                        mbar_arrive(&tail_ready[st]);
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        const uint32_t taddr0 = tmem_base + ((uint32_t)(q * 32) << 16);
+        const uint32_t stg_w = smem_addr(smem + p.off_out) + (uint32_t)q * (uint32_t)p.out_slots * RAGGED_SLOT_BYTES;
+        const bool bf16 = p.out_type == RAGGED_OUT_BF16;
+        uint32_t tile_it = 0, slot = 0;
+        for (int t = t_first; t < num_tiles; t += t_stride) {
+            const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+            const bool zero = ti.nkb == 0; // TN: a group without rows
+            if (zero && p.accumulate)
+                continue;
+            const uint32_t buf = tile_it & 1;
+            if (!zero) {
+                const bool got = wait_ragged(&acc_full[buf], (tile_it >> 1) & 1, abort_flag, p);
+                if (!__all_sync(0xffffffffu, got))
+                    break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = taddr0 + buf * (uint32_t)BN;
+            const int i0 = ti.i0 + (PAIR ? (int)rank * 128 : 0) + q * 32; // this warp's first X row
+            if constexpr (SWAP) {
+                // a lane owns output column i0 + lane and the tile's token
+                // rows: 32 lanes store 64 consecutive bytes of a row
+                const int col = i0 + lane;
+                const int tok = min(BN, ti.rows - ti.j0);
+                uint16_t *dst = static_cast<uint16_t *>(p.d) + (size_t)(ti.first + ti.j0) * p.d_cols + col;
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) {
+                    if (c >= tok)
+                        break;
+                    float v[32];
+                    tmem_ld32(taddr + c, v);
+                    tmem_wait_ld(v);
+                    if (col < p.d_cols) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c + j < tok)
+                                dst[(size_t)(c + j) * p.d_cols] = (uint16_t)pack_16x2(v[j], 0.0f, bf16);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&acc_empty[buf]);
+                ++tile_it;
+                continue;
+            }
+            // rows of this warp that are stored: a segment may end inside the
+            // tile (NT, NN); TN clips at the tensor's edge
+            const int left = TN ? 32 : ti.rows - i0;
+            const bool whole = TN || left >= 32;
+            if (left <= 0) { // none: the warp hands the accumulator back unread
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR && !leader)
+                        mbar_arrive_cluster(map_shared_rank(smem_addr(&acc_empty[buf]), 0u));
+                    else
+                        mbar_arrive(&acc_empty[buf]);
+                }
+                ++tile_it;
+                continue;
+            }
+            const bool f32 = TN && p.out_type == RAGGED_OUT_F32;
+            const int row = TN ? i0 : ti.first + i0;
+            const int width = f32 ? 32 : 64; // columns per 128-byte staged row
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 64) {
+                float v[2][32];
+                if (zero) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[0][j] = v[1][j] = 0.0f;
+                } else {
+                    tmem_ld32(taddr + c, v[0]);
+                    tmem_ld32(taddr + c + 32, v[1]);
+                    tmem_wait_ld(v[0]);
+                    reg_tie32(v[1]);
+                    if (c + 64 == BN) { // the accumulator has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR && !leader)
+                                mbar_arrive_cluster(map_shared_rank(smem_addr(&acc_empty[buf]), 0u));
+                            else
+                                mbar_arrive(&acc_empty[buf]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!f32 && h == 1)
+                        break;
+                    const int col = ti.j0 + c + h * 32;
+                    // the slot's last store has read it
+                    if (lane == 0) {
+                        if (p.out_slots == 2)
+                            bulk_wait_read_1();
+                        else
+                            bulk_wait_read_all();
+                    }
+                    __syncwarp();
+                    const uint32_t stg = stg_w + slot * RAGGED_SLOT_BYTES;
+                    const uint32_t line = stg + lane * 128;
+                    // 16-byte piece i of row r sits at piece i ^ (r % 8): TMA's 128-byte swizzle
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t at = line + ((i ^ (lane & 7)) << 4);
+                        if (f32) {
+                            st_shared_v4(at, __float_as_uint(v[h][4 * i]), __float_as_uint(v[h][4 * i + 1]),
+                                         __float_as_uint(v[h][4 * i + 2]), __float_as_uint(v[h][4 * i + 3]));
+                        } else {
+                            const float *w = &v[i >> 2][(i & 3) * 8];
+                            st_shared_v4(at, pack_16x2(w[0], w[1], bf16), pack_16x2(w[2], w[3], bf16),
+                                         pack_16x2(w[4], w[5], bf16), pack_16x2(w[6], w[7], bf16));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (whole) {
+                        if (lane == 0) {
+                            if (col < p.d_cols && (!TN || row < p.d_rows)) {
+                                if constexpr (TN) {
+                                    if (p.accumulate)
+                                        tma_add_3d(&tmap_d, stg, col, row, ti.g);
+                                    else
+                                        tma_store_3d(&tmap_d, stg, col, row, ti.g);
+                                } else {
+                                    tma_store_2d(&tmap_d, stg, col, row);
+                                }
+                            }
+                            bulk_commit_group();
+                        }
+                    } else {
+                        // a segment's last rows: 8 lanes store a row's 128 bytes
+                        const int piece = lane & 7;
+#pragma unroll 1
+                        for (int r = lane >> 3; r < left; r += 4) {
+                            const uint4 w = ld_shared_v4(stg + r * 128 + ((piece ^ (r & 7)) << 4));
+                            if (col + piece * 8 < p.d_cols)
+                                st_global_v4(static_cast<uint16_t *>(p.d) + (size_t)(row + r) * p.d_cols + col +
+                                                 piece * 8,
+                                             w.x, w.y, w.z, w.w);
+                        }
+                        if (lane == 0)
+                            bulk_commit_group(); // empty: keeps one group per slot use
+                    }
+                    __syncwarp();
+                    slot = slot + 1 == (uint32_t)p.out_slots ? 0 : slot + 1;
+                    if (width == 64)
+                        break;
+                }
+            }
+            if (!zero)
+                ++tile_it;
+        }
+        // every store has completed before the CTA exits
+        if (lane == 0)
+            bulk_wait_all();
+    }
+
+    __syncwarp();
+    if constexpr (PAIR)
+        cluster_sync(); // neither CTA leaves while its pair may still use its memory
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem_base, T::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, T::TMEM_COLS);
+    }
+}
+
+} // namespace fp8nt

@@ -514,6 +514,85 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// Tiled load of 2 coordinates (x, y), or 3 with the group g, into this CTA's
+// shared memory; completion is counted on the barrier at cluster address
+// `bar`, which is the pair leader's with LEADER.
+template <bool THREE, bool LEADER>
+__device__ __forceinline__ void tma_load_nd(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t g)
+{
+    if constexpr (THREE && LEADER)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(g)
+            : "memory");
+    else if constexpr (THREE)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(g)
+            : "memory");
+    else if constexpr (LEADER)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+}
+
+// 3-D tiled FP32 addition to global memory (bulk-group completion); elements
+// outside the tensor are not touched.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src_smem, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src_smem), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// Wait until all but the newest of this thread's committed bulk stores have
+// read their shared-memory sources.
+__device__ __forceinline__ void bulk_wait_read_1()
+{
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+// D(tmem) (+)= X(smem) * Y(smem)^T, 16-bit operands -> FP32; PAIR: over both
+// CTAs of a pair, issued by its leader.
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t x_desc, uint64_t y_desc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(x_desc), "l"(y_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(x_desc), "l"(y_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Arrive on a barrier of another CTA of the cluster, releasing this thread's
+// earlier shared-memory writes to it.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // ---------------------------------------------------------------- stores
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)

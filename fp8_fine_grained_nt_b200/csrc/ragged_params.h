@@ -1,0 +1,66 @@
+// Parameters and shared-memory plan of the ragged grouped products
+// (kernel_ragged.cuh), shared by the host launcher and the kernel.
+#pragma once
+
+#include <stdint.h>
+
+#include "params.h"
+
+namespace fp8nt {
+
+enum RaggedDir : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2 };
+enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 = 2 };
+
+constexpr int RAGGED_BK = 64;           // reduction elements per stage: 128-byte swizzled rows
+constexpr int RAGGED_THREADS = 256;     // 8 warps
+constexpr int RAGGED_MAX_STAGES = 12;
+constexpr int RAGGED_MAX_GROUPS = 1024;
+constexpr uint32_t RAGGED_SLOT_BYTES = 4096; // output staging: 32 rows of 128 bytes
+
+struct RaggedParams {
+    const int *offsets; // [num_groups + 1] segment bounds
+    void *d;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    int num_groups;
+    int total_rows;      // rows of the token tensors
+    int d_rows;          // TN: rows of one group's result (N)
+    int d_cols;          // columns of the result
+    int nkb;             // NT, NN: 64-wide blocks of the reduction
+    int x_blocks;        // SWAP: blocks of 128 output columns; TN: blocks of X rows
+    int y_blocks;        // NT, NN without SWAP: blocks of output columns; TN: blocks of Y rows
+    int tiles_per_group; // TN
+    int out_type;        // RaggedOut
+    int accumulate;      // TN into FP32: add to the result
+    uint32_t idesc;      // tcgen05.mma instruction descriptor
+    int stages;
+    int out_slots;       // staging slots per epilogue warp (0 with SWAP)
+    uint32_t off_out;
+    uint32_t off_groups; // tile prefix [G + 1], first row [G], rows [G]
+    uint32_t off_bars;
+    uint32_t off_misc;   // tensor-memory address, abort flag, scan partials
+    uint32_t total;      // bytes, excluding the 1024-byte alignment slack
+};
+
+// Operand ring of `stages`, staging, group table, barriers.
+inline void make_ragged_plan(RaggedParams &p, uint32_t stage_bytes, int stages, int out_slots)
+{
+    p.stages = stages;
+    p.out_slots = out_slots;
+    p.off_out = stage_bytes * (uint32_t)stages;
+    p.off_groups = p.off_out + 4u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
+    p.off_bars = align_up_u32(p.off_groups + 4u * (3u * (uint32_t)p.num_groups + 1u), 8);
+    p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 5u), 16);
+    p.total = p.off_misc + 64;
+}
+
+// tcgen05.mma kind::f16: FP32 result, both operands BF16 (or FP16), `mn` set
+// where the operand's i / j index is the contiguous one, M x N per MMA.
+inline uint32_t ragged_idesc(bool bf16, bool x_mn, bool y_mn, int m, int n)
+{
+    const uint32_t type = bf16 ? 1u : 0u;
+    return (1u << 4) | (type << 7) | (type << 10) | ((x_mn ? 1u : 0u) << 15) | ((y_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+} // namespace fp8nt

@@ -129,9 +129,48 @@ int m_grouped_gemm_fp8_fp8_bf16_nt_masked(const void *A, const float *sa, const 
  * point reads (columns M..ld-1 are not written).  x must be finite.
  * K % 128 == 0; pointers 16-byte aligned device memory owned by the caller;
  * M == 0 does nothing. */
-enum { DG_INPUT_F32 = 0, DG_INPUT_BF16 = 1 };
+enum { DG_INPUT_F32 = 0, DG_INPUT_BF16 = 1, DG_INPUT_F16 = 2 };
 int quantize_fp8_1x128(const void *x, int x_dtype, void *q, float *sa, int M, int K,
                        dg_stream_t stream);
+
+/* Grouped products over ragged segments, 16-bit operands
+ * --------------------------------------------------------
+ * The three products of a grouped (mixture-of-experts) linear layer whose
+ * weights are kept in BF16 or FP16: forward, input gradient and weight
+ * gradient.  Group g owns rows [offsets[g], offsets[g + 1]) of the token
+ * tensors; segments have any length, zero included, and start at any row, so
+ * no padding rows are needed.  Rows outside every segment are neither written
+ * nor do they take part in a sum, whatever they hold.
+ *   dtype    DG_INPUT_BF16 or DG_INPUT_F16: type of A and B (and of D, except
+ *            where d_dtype says otherwise).
+ *   offsets  [num_groups + 1] int32 on the device (4-byte aligned; never read
+ *            by the host), ascending, within [0, M_sum].  A value that is not
+ *            sets DG_ERR_DEVICE_BAD_INDEX and is clamped to [0, M_sum] and to
+ *            the segment's start.
+ * Everything row-major and dense; N % 8 == 0, K % 8 == 0 (16-byte rows),
+ * 1 <= num_groups <= 1024, M_sum >= 0.  Sums are FP32 over the whole
+ * reduction, rounded once (to nearest even) to D's type.  D must not overlap
+ * A or B. */
+
+/* Forward: D[t,n] = sum_k A[t,k] * B[g,n,k] for t in segment g.
+ *   A [M_sum,K]   B [num_groups,N,K]   D [M_sum,N] */
+int m_grouped_gemm_nt_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype,
+                             int num_groups, int M_sum, int N, int K, dg_stream_t stream);
+
+/* Input gradient: D[t,k] = sum_n A[t,n] * B[g,n,k] for t in segment g (A holds
+ * the gradients of the forward's output, B the forward's weights as they are).
+ *   A [M_sum,N]   B [num_groups,N,K]   D [M_sum,K] */
+int m_grouped_gemm_nn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype,
+                             int num_groups, int M_sum, int N, int K, dg_stream_t stream);
+
+/* Weight gradient: D[g,n,k] = sum over t in segment g of A[t,n] * B[t,k] (A
+ * holds the gradients of the forward's output, B the forward's input).
+ *   A [M_sum,N]   B [M_sum,K]   D [num_groups,N,K]
+ * d_dtype: DG_INPUT_F32, or dtype.  accumulate != 0 adds to D (FP32 only);
+ * else D is written in full, with zeros for a group without rows. */
+int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype,
+                             int d_dtype, int accumulate, int num_groups, int M_sum, int N, int K,
+                             dg_stream_t stream);
 
 /* Row alignment of each expert segment in the contiguous layout (DeepGEMM
  * README, utility functions: get_m_alignment_for_contiguous_layout).  128. */
@@ -233,6 +272,14 @@ int dg_force_swap_ab(int mode);
  * block layout allows it and the cycle estimate favours it.  Returns DG_OK,
  * or DG_ERR_INVALID_ARGUMENT for another mode. */
 int dg_force_tail_split(int mode);
+
+/* Test hook: pin the tile form of later ragged grouped calls for which a
+ * kernel of that form is built (0, 0, 0 = automatic choice): swap_ab 1 = the
+ * weights on the MMA's 128-row side and block_n (32, 64 or 128) token rows
+ * per tile; cta_pair 1 = 256 x 256 tiles by CTA pairs; block_n alone = one
+ * CTA per tile of 128 x block_n.  Returns DG_ERR_UNSUPPORTED_SHAPE if no
+ * direction has such a kernel. */
+int dg_force_ragged(int swap_ab, int cta_pair, int block_n);
 
 #ifdef __cplusplus
 }
