@@ -28,6 +28,11 @@ __all__ = [
     "m_grouped_gemm_nt_ragged",
     "m_grouped_gemm_nn_ragged",
     "k_grouped_gemm_tn_ragged",
+    "group_rows_by_index",
+    "get_row_groups_capacity",
+    "get_group_rows_workspace_size",
+    "m_grouped_lora_add",
+    "get_lora_workspace_size",
     "get_m_alignment_for_contiguous_layout",
     "get_tma_aligned_size",
     "get_col_major_tma_aligned_tensor",
@@ -109,6 +114,15 @@ def load_library():
         lib.m_grouped_gemm_nt_ragged.argtypes = [P, P, P, P, I, I, I, I, I, P]
         lib.m_grouped_gemm_nn_ragged.argtypes = [P, P, P, P, I, I, I, I, I, P]
         lib.k_grouped_gemm_tn_ragged.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P]
+        Z, L = ctypes.c_size_t, ctypes.c_longlong
+        lib.group_rows_by_index.argtypes = [P, I, P, P, P, P, I, I, I, P, Z, P]
+        lib.get_row_groups_capacity.argtypes = [I, I, I]
+        lib.get_group_rows_workspace_size.argtypes = [I, I]
+        lib.get_group_rows_workspace_size.restype = L
+        lib.m_grouped_lora_add.argtypes = [P, L, P, P, P, P, L, P, L, P, P, I, I, I, I, I, I, I, P,
+                                           Z, P]
+        lib.get_lora_workspace_size.argtypes = [I, I, I, I]
+        lib.get_lora_workspace_size.restype = L
         lib.dg_force_ragged.argtypes = [I, I, I]
         _lib = lib
         return lib
@@ -332,6 +346,123 @@ def k_grouped_gemm_tn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
             else _dev(d, "d", _F32, 3), _dev(offsets, "offsets", _I32, 1))
     _call("k_grouped_gemm_tn_ragged", stream, _same_device(a, b, d, offsets), *args,
           _DTYPE_CODE[a.dtype], _DTYPE_CODE[d.dtype], int(accumulate), G, a.shape[0], N, K)
+    return d
+
+
+def _workspace(given, need: int, stream, device: torch.device):
+    """(pointer, bytes, owner) of the caller's workspace, or of one from torch's
+    allocator that belongs to the stream the call runs on."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if need == 0:
+        return 0, 0, None
+    if stream is None:
+        own = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            own = torch.empty(need, dtype=torch.uint8, device=device)
+    return own.data_ptr(), need, own
+
+
+def _size(name: str, *args: int) -> int:
+    n = getattr(_lib or load_library(), name)(*args)
+    if n < 0:
+        raise Fp8NtError(-n, name)
+    return n
+
+
+def get_row_groups_capacity(num_rows: int, num_groups: int, alignment: int = 1) -> int:
+    """Slots that num_rows rows in num_groups groups can need (length of order and m_indices)."""
+    return _size("get_row_groups_capacity", int(num_rows), int(num_groups), int(alignment))
+
+
+def get_group_rows_workspace_size(num_rows: int, num_groups: int) -> int:
+    """Bytes of workspace group_rows_by_index needs (0 for short calls)."""
+    return _size("get_group_rows_workspace_size", int(num_rows), int(num_groups))
+
+
+def group_rows_by_index(index: torch.Tensor, num_groups: int, offsets: torch.Tensor,
+                        order: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                        m_indices: Optional[torch.Tensor] = None, alignment: int = 1,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Rows sorted (stably) by the group each belongs to; the grouped calls' layout.
+
+    index: [R] int32 or int64, the group of each row or -1 for none.  Results
+    (int32): offsets [num_groups+1], the first slot of each segment (multiples of
+    alignment); order [capacity], the row in each slot or -1; slots [R], the slot
+    of each row or -1 (optional); m_indices [capacity], the group of each slot or
+    -1 (optional); capacity = get_row_groups_capacity(R, num_groups, alignment).
+    Returns (offsets, order, slots, m_indices).
+    """
+    R = index.shape[0]
+    cap = get_row_groups_capacity(R, num_groups, alignment)
+    args = (_dev(index, "index", (torch.int32, torch.int64), 1), 1 if index.dtype == torch.int64 else 0,
+            _dev(offsets, "offsets", _I32, 1), _dev(order, "order", _I32, 1),
+            None if slots is None else _dev(slots, "slots", _I32, 1),
+            None if m_indices is None else _dev(m_indices, "m_indices", _I32, 1))
+    if (offsets.shape[0] != num_groups + 1 or order.shape[0] != cap
+            or (slots is not None and slots.shape[0] != R)
+            or (m_indices is not None and m_indices.shape[0] != cap)):
+        raise ValueError(f"offsets must hold {num_groups + 1} values, order and m_indices {cap}, slots {R}")
+    device = _same_device(*(t for t in (index, offsets, order, slots, m_indices) if t is not None))
+    ptr, size, _own = _workspace(workspace, get_group_rows_workspace_size(R, num_groups), stream, device)
+    _call("group_rows_by_index", stream, device, *args, R, num_groups, alignment, ptr, size)
+    return offsets, order, slots, m_indices
+
+
+def get_lora_workspace_size(num_slots: int, rank: int, N: int, K: int) -> int:
+    """Bytes of workspace m_grouped_lora_add needs."""
+    return _size("get_lora_workspace_size", int(num_slots), int(rank), int(N), int(K))
+
+
+def _rows(t: torch.Tensor, name: str, dtypes) -> tuple[int, int]:
+    """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def m_grouped_lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                       scales: torch.Tensor, c: torch.Tensor, d: torch.Tensor,
+                       m_indices: torch.Tensor, order: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection c:
+    d[t] = c[t] + scales[g] (x[t] lora_a[g]^T) lora_b[g]^T.
+
+    x: [T,K]; lora_a: [L,R,K]; lora_b: [L,N,R]; c, d: [T,N] (d may be c), all bf16
+    or all fp16; x, c and d may be column ranges of wider tensors; scales: [L] fp32;
+    m_indices: [S] int32, adapter g of each slot (-1: none); order: [S] int32, row t
+    of each slot (each row at most once; default: slot i is row i).  Rows in no
+    slot with an adapter are not written.  Slots sorted by adapter
+    (group_rows_by_index) share the reads of its weights.
+    """
+    L, R, K = lora_a.shape
+    (T, N), S = d.shape, m_indices.shape[0]
+    if (x.shape[0] != T or x.shape[1] != K or tuple(lora_b.shape) != (L, N, R) or tuple(c.shape) != (T, N)
+            or scales.shape[0] != L or (order is not None and order.shape[0] != S)):
+        raise ValueError("shape mismatch between x, lora_a, lora_b, scales, c, d, m_indices and order")
+    if order is None and S > T:
+        raise ValueError(f"m_indices holds {S} slots for {T} rows")
+    dtypes = (x.dtype,) if x.dtype in _HALF else _HALF
+    args = (*_rows(x, "x", dtypes), _dev(lora_a, "lora_a", dtypes, 3), _dev(lora_b, "lora_b", dtypes, 3),
+            _dev(scales, "scales", _F32, 1), *_rows(c, "c", dtypes), *_rows(d, "d", dtypes),
+            _dev(m_indices, "m_indices", _I32, 1), None if order is None else _dev(order, "order", _I32, 1))
+    device = _same_device(x, lora_a, lora_b, scales, c, d, m_indices)
+    if order is not None:
+        _same_device(x, order)
+    ptr, size, _own = _workspace(workspace, get_lora_workspace_size(S, R, N, K), stream, device)
+    _call("m_grouped_lora_add", stream, device, *args, _DTYPE_CODE[x.dtype], S, T, L, R, N, K, ptr, size)
     return d
 
 

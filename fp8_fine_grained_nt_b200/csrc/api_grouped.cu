@@ -32,6 +32,8 @@ std::atomic<uint32_t> g_forced_ragged{0};
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
+constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, with room to round up
+
 // The kernel of a call.
 const RaggedKernel *choose_ragged(int dir, int groups, int rows, int N, int K)
 {
@@ -95,8 +97,8 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     if (st != DG_OK)
         return st;
     const bool tn = dir == RAGGED_TN;
-    if (M_sum == 0) {
-        if (!tn || accumulate)
+    if (M_sum == 0) { // the weight gradient of no rows
+        if (accumulate)
             return DG_OK;
         const size_t bytes = (size_t)G * N * K * (d_type == RAGGED_OUT_F32 ? 4 : 2);
         return cudaMemsetAsync(D, 0, bytes, stream) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
@@ -220,18 +222,20 @@ int m_grouped_gemm_nt_ragged(const void *A, const void *B, void *D, const int *o
                              int M_sum, int N, int K, dg_stream_t stream)
 {
     const int st = check_ragged(RAGGED_NT, A, B, D, offsets, dtype, num_groups, M_sum, N, K);
-    return st != DG_OK ? st
-                       : run_ragged(RAGGED_NT, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
-                                    reinterpret_cast<cudaStream_t>(stream));
+    if (st != DG_OK || M_sum == 0)
+        return st;
+    return run_ragged(RAGGED_NT, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 int m_grouped_gemm_nn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype, int num_groups,
                              int M_sum, int N, int K, dg_stream_t stream)
 {
     const int st = check_ragged(RAGGED_NN, A, B, D, offsets, dtype, num_groups, M_sum, N, K);
-    return st != DG_OK ? st
-                       : run_ragged(RAGGED_NN, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
-                                    reinterpret_cast<cudaStream_t>(stream));
+    if (st != DG_OK || M_sum == 0)
+        return st;
+    return run_ragged(RAGGED_NN, A, B, D, offsets, dtype, dtype, 0, num_groups, M_sum, N, K,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype, int d_dtype,
@@ -246,6 +250,121 @@ int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *o
         return DG_ERR_INVALID_ARGUMENT;
     return run_ragged(RAGGED_TN, A, B, D, offsets, dtype, d_dtype, accumulate != 0, num_groups, M_sum, N, K,
                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+int get_row_groups_capacity(int num_rows, int num_groups, int alignment)
+{
+    if (num_rows < 0 || num_groups <= 0 || alignment <= 0)
+        return -DG_ERR_INVALID_ARGUMENT;
+    const long most = num_rows < num_groups ? num_rows : num_groups; // groups with rows
+    const long cap = (num_rows + most * (long)(alignment - 1) + alignment - 1) / alignment * alignment;
+    return cap > kMaxSlots ? -DG_ERR_UNSUPPORTED_SHAPE : (int)cap;
+}
+
+long long get_group_rows_workspace_size(int num_rows, int num_groups)
+{
+    if (num_rows < 0 || num_groups <= 0)
+        return -DG_ERR_INVALID_ARGUMENT;
+    if (num_groups > RAGGED_MAX_GROUPS || num_rows > kMaxSlots)
+        return -DG_ERR_UNSUPPORTED_SHAPE;
+    const long chunks = ceil_div(num_rows, group_rows_chunk(num_rows));
+    return chunks > 1 ? (long long)chunks * num_groups * 4 : 0;
+}
+
+int group_rows_by_index(const void *index, int index_dtype, int *offsets, int *order, int *slots, int *m_indices,
+                        int num_rows, int num_groups, int alignment, void *workspace, size_t workspace_bytes,
+                        dg_stream_t stream)
+{
+    if (index_dtype != DG_INDEX_I32 && index_dtype != DG_INDEX_I64)
+        return DG_ERR_INVALID_ARGUMENT;
+    const int capacity = get_row_groups_capacity(num_rows, num_groups, alignment);
+    if (capacity < 0)
+        return -capacity;
+    const long long need = get_group_rows_workspace_size(num_rows, num_groups);
+    if (need < 0)
+        return (int)-need;
+    if (!offsets || (num_rows > 0 && (!index || !order)) || (need > 0 && !workspace) ||
+        (long long)workspace_bytes < need)
+        return DG_ERR_INVALID_ARGUMENT;
+    if (!aligned(index, index_dtype == DG_INDEX_I64 ? 8 : 4) || !aligned(offsets, 4) || !aligned(order, 4) ||
+        !aligned(slots, 4) || !aligned(m_indices, 4) || !aligned(workspace, 4))
+        return DG_ERR_MISALIGNED;
+    DeviceView dev;
+    const int st = current_device(&dev);
+    if (st != DG_OK)
+        return st;
+    return launch_group_rows(index, index_dtype == DG_INDEX_I64, num_rows, num_groups, alignment, capacity, offsets,
+                             order, slots, m_indices, static_cast<int *>(workspace), dev.status, dev.index,
+                             reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? DG_OK
+               : DG_ERR_CUDA;
+}
+
+long long get_lora_workspace_size(int num_slots, int rank, int N, int K)
+{
+    if (num_slots < 0 || rank < 0 || N < 0 || K < 0)
+        return -DG_ERR_INVALID_ARGUMENT;
+    if (num_slots > kMaxSlots || rank == 0 || rank > LORA_MAX_RANK || rank % 8 != 0 || N == 0 || N % 8 != 0 || K == 0 ||
+        K % 8 != 0)
+        return -DG_ERR_UNSUPPORTED_SHAPE;
+    return (long long)lora_plan(num_slots, rank, N, K).splits * num_slots * rank * 4;
+}
+
+int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const void *lora_b, const float *scales,
+                       const void *c, long long ld_c, void *d, long long ld_d, const int *m_indices, const int *order,
+                       int dtype, int num_slots, int num_rows, int num_adapters, int rank, int N, int K,
+                       void *workspace, size_t workspace_bytes, dg_stream_t stream)
+{
+    if ((dtype != DG_INPUT_BF16 && dtype != DG_INPUT_F16) || num_rows < 0 || num_adapters <= 0)
+        return DG_ERR_INVALID_ARGUMENT;
+    const long long need = get_lora_workspace_size(num_slots, rank, N, K);
+    if (need < 0)
+        return (int)-need;
+    if (ld_x < K || ld_c < N || ld_d < N)
+        return DG_ERR_INVALID_ARGUMENT;
+    if (ld_x % 8 != 0 || ld_c % 8 != 0 || ld_d % 8 != 0)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    if (num_slots == 0 || num_rows == 0)
+        return DG_OK;
+    if (!x || !lora_a || !lora_b || !scales || !c || !d || !m_indices || !workspace ||
+        (long long)workspace_bytes < need)
+        return DG_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(c, 16) || !aligned(d, 16) ||
+        !aligned(workspace, 16) || !aligned(scales, 4) || !aligned(m_indices, 4) || !aligned(order, 4))
+        return DG_ERR_MISALIGNED;
+    DeviceView dev;
+    const int st = current_device(&dev);
+    if (st != DG_OK)
+        return st;
+    LoraPlan plan = lora_plan(num_slots, rank, N, K);
+    plan.device = dev.index;
+    LoraParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = x;
+    p.lora_a = lora_a;
+    p.lora_b = lora_b;
+    p.scales = scales;
+    p.c = c;
+    p.d = d;
+    p.m_indices = m_indices;
+    p.order = order;
+    p.v = static_cast<float *>(workspace);
+    p.status = dev.status;
+    p.ld_x = (long)ld_x;
+    p.ld_c = (long)ld_c;
+    p.ld_d = (long)ld_d;
+    p.slots = num_slots;
+    p.rows = num_rows;
+    p.adapters = num_adapters;
+    p.R = rank;
+    p.N = N;
+    p.K = K;
+    p.k_chunk = plan.k_chunk;
+    p.splits = plan.splits;
+    p.n_chunk = plan.n_chunk;
+    return launch_lora(p, plan, dtype == DG_INPUT_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? DG_OK
+               : DG_ERR_CUDA;
 }
 
 int dg_force_ragged(int swap_ab, int cta_pair, int block_n)

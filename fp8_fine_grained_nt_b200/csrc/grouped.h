@@ -43,4 +43,40 @@ typedef cudaError_t (*RaggedLaunchFn)(const RaggedLaunchArgs &);
 #include "ragged.def"
 #undef FP8NT_RAGGED
 
+// Rows grouped by index (csrc/group_rows.cu).  chunk: rows that one CTA takes;
+// with more than one chunk, `counts` holds [chunks][groups] ints.
+int group_rows_chunk(int rows);
+cudaError_t launch_group_rows(const void *index, bool i64, int rows, int groups, int alignment, int capacity,
+                              int *offsets, int *order, int *slots, int *m_indices, int *counts, unsigned int *status,
+                              int device, cudaStream_t stream);
+
+// Low-rank adapters (csrc/lora.cu).
+constexpr int LORA_MAX_RANK = 256;
+
+struct LoraParams {
+    const void *x; // [rows][ld_x]
+    const void *lora_a;
+    const void *lora_b;
+    const float *scales;
+    const void *c; // [rows][ld_c]
+    void *d;       // [rows][ld_d]
+    const int *m_indices;
+    const int *order; // null: slot i is row i
+    float *v;         // [splits][slots][R]
+    unsigned int *status;
+    long ld_x, ld_c, ld_d;
+    int slots, rows, adapters, R, N, K;
+    int k_chunk, splits; // k per CTA of the first kernel, and how many such ranges
+    int n_chunk;         // columns per CTA of the second
+};
+
+struct LoraPlan {
+    int device;
+    bool wide;
+    int k_chunk, splits, n_chunk;
+};
+
+LoraPlan lora_plan(int slots, int R, int N, int K);
+cudaError_t launch_lora(const LoraParams &p, const LoraPlan &plan, bool bf16, cudaStream_t stream);
+
 } // namespace fp8nt

@@ -43,6 +43,8 @@
 #ifndef FP8_NT_H
 #define FP8_NT_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -171,6 +173,75 @@ int m_grouped_gemm_nn_ragged(const void *A, const void *B, void *D, const int *o
 int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *offsets, int dtype,
                              int d_dtype, int accumulate, int num_groups, int M_sum, int N, int K,
                              dg_stream_t stream);
+
+/* Rows grouped by an index: the layout the grouped calls read, built on the
+ * device from the group of each row (a router's choice, a request's adapter).
+ *   index      [num_rows] DG_INDEX_I32 or DG_INDEX_I64: 0..num_groups-1, or -1
+ *              for a row without a group.  Any other value sets
+ *              DG_ERR_DEVICE_BAD_INDEX and counts as -1.
+ *   alignment  >= 1: every segment starts at a multiple of it and is padded to
+ *              one (1: exact segments, as the ragged calls read them;
+ *              get_m_alignment_for_contiguous_layout(): as the contiguous FP8
+ *              form reads them).
+ * Results, all int32 (4-byte aligned):
+ *   offsets    [num_groups + 1] first slot of each segment; the last is the end
+ *   order      [capacity] row in each slot, -1 in slots without one (padding,
+ *              and everything from offsets[num_groups] on).  Rows of a group
+ *              keep their order.
+ *   slots      [num_rows] slot of each row, -1 if it has none; may be NULL
+ *   m_indices  [capacity] group of each slot, -1 in slots without a row; may
+ *              be NULL
+ * with capacity = get_row_groups_capacity(num_rows, num_groups, alignment), the
+ * most slots the rows can need.  workspace: at least
+ * get_group_rows_workspace_size(num_rows, num_groups) bytes of device memory
+ * (0 for short calls; 4-byte aligned), in use until the call's work has
+ * completed; calls that may run at the same time need one each.
+ * num_groups <= 1024, num_rows and capacity <= 2^30. */
+enum { DG_INDEX_I32 = 0, DG_INDEX_I64 = 1 };
+int group_rows_by_index(const void *index, int index_dtype, int *offsets, int *order, int *slots,
+                        int *m_indices, int num_rows, int num_groups, int alignment,
+                        void *workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* Slots that num_rows rows in num_groups groups can need; negative dg_status
+ * on a bad argument. */
+int get_row_groups_capacity(int num_rows, int num_groups, int alignment);
+
+/* Bytes of workspace group_rows_by_index needs; negative dg_status on a bad
+ * argument. */
+long long get_group_rows_workspace_size(int num_rows, int num_groups);
+
+/* Low-rank adapters of many requests beside a shared projection (whose result,
+ * e.g. a dense FP8 GEMM's D, is C).  For slot i with adapter g = m_indices[i]
+ * and row t = order[i] (t = i if order is NULL):
+ *   D[t,n] = C[t,n] + scales[g] * sum_r ( sum_k X[t,k] A[g,r,k] ) B[g,n,r]
+ * with FP32 sums throughout (the inner sums are not rounded to 16 bits) and
+ * one rounding to D's type (to nearest even).
+ *   X [num_rows] rows of K   A [num_adapters,rank,K]   C, D [num_rows] rows of N
+ *   B [num_adapters,N,rank]  scales [num_adapters] FP32
+ * all but scales of type dtype (DG_INPUT_BF16 or DG_INPUT_F16).  ld_x, ld_c,
+ * ld_d: row strides in elements (multiples of 8), so that X, C and D may be
+ * column ranges of wider tensors; A and B are dense.  D may be C (in place),
+ * but must not overlap it otherwise, nor X, A or B.
+ *   m_indices [num_slots] int32 adapter of each slot, -1 for none: its row is
+ *             not written (nor is a row in no slot).
+ *   order     [num_slots] int32 row of each slot (-1: none); each row at most
+ *             once.  Slots of the same adapter next to each other (as
+ *             group_rows_by_index orders them) share the reads of its weights.
+ * A value out of range sets DG_ERR_DEVICE_BAD_INDEX and its slot is skipped.
+ * rank: a multiple of 8, at most 256 (smaller adapters: zero rows of A and
+ * columns of B); N % 8 == 0, K % 8 == 0.  workspace: at least
+ * get_lora_workspace_size(num_slots, rank, N, K) bytes, 16-byte aligned, in use
+ * until the call's work has completed; calls that may run at the same time
+ * need one each. */
+int m_grouped_lora_add(const void *X, long long ld_x, const void *A, const void *B,
+                       const float *scales, const void *C, long long ld_c, void *D, long long ld_d,
+                       const int *m_indices, const int *order, int dtype, int num_slots,
+                       int num_rows, int num_adapters, int rank, int N, int K, void *workspace,
+                       size_t workspace_bytes, dg_stream_t stream);
+
+/* Bytes of workspace m_grouped_lora_add needs; negative dg_status on a bad
+ * argument. */
+long long get_lora_workspace_size(int num_slots, int rank, int N, int K);
 
 /* Row alignment of each expert segment in the contiguous layout (DeepGEMM
  * README, utility functions: get_m_alignment_for_contiguous_layout).  128. */
