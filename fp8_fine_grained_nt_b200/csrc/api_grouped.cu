@@ -336,8 +336,7 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
     const int st = current_device(&dev);
     if (st != DG_OK)
         return st;
-    LoraPlan plan = lora_plan(num_slots, rank, N, K);
-    plan.device = dev.index;
+    const LoraPlan plan = lora_plan(num_slots, rank, N, K);
     LoraParams p;
     memset(&p, 0, sizeof(p));
     p.x = x;
@@ -362,7 +361,7 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
     p.k_chunk = plan.k_chunk;
     p.splits = plan.splits;
     p.n_chunk = plan.n_chunk;
-    return launch_lora(p, plan, dtype == DG_INPUT_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_lora(p, dtype == DG_INPUT_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DG_OK
                : DG_ERR_CUDA;
 }

@@ -71,12 +71,10 @@ struct LoraParams {
 };
 
 struct LoraPlan {
-    int device;
-    bool wide;
     int k_chunk, splits, n_chunk;
 };
 
 LoraPlan lora_plan(int slots, int R, int N, int K);
-cudaError_t launch_lora(const LoraParams &p, const LoraPlan &plan, bool bf16, cudaStream_t stream);
+cudaError_t launch_lora(const LoraParams &p, bool bf16, cudaStream_t stream);
 
 } // namespace fp8nt

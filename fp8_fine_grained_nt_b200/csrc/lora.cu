@@ -34,6 +34,8 @@ namespace {
 
 constexpr int LORA_THREADS = 256;
 constexpr int LORA_WARPS = 8;
+constexpr int LORA_SLOTS = 16;   // slots per CTA of the first kernel: one MMA's rows
+constexpr int LORA_UP_SLOTS = 8; // of the second
 
 // 16 x 8 += 16 x 16 * (8 x 16)^T, 16-bit operands, FP32 sums
 template <bool BF16>
@@ -104,32 +106,29 @@ __device__ __forceinline__ uint32_t segment_starts(int adapter, int lane, int n)
 
 // ---------------------------------------------------------------- down
 
-// MT blocks of 16 slots per warp job, NT blocks of 8 ranks, WR groups of
-// 16 * MT slots per CTA; the CTA's 8 / WR warps of a group share its k range.
-template <bool BF16, int MT, int NT, int WR>
+// 16 slots, 8 NT ranks and one k range per CTA; a warp's job is one segment and
+// a slice of the range (all of it once there are 8 segments or more).
+template <bool BF16, int NT>
 __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParams p)
 {
-    constexpr int SB = 16 * MT;         // slots of a group
-    constexpr int WK = LORA_WARPS / WR; // warps of a group
-    constexpr int RB = 8 * NT;          // ranks of this CTA
-    extern __shared__ float red[];      // [WR][WK][SB][RB]
+    constexpr int SB = LORA_SLOTS;
+    constexpr int RB = 8 * NT; // ranks of this CTA
+    __shared__ float4 red[LORA_WARPS * SB * RB / 4]; // [slice][slot][rank]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wr = warp / WK, wk = warp % WK;
     const int t = lane & 3, q = lane >> 2;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int slot0 = (blockIdx.x * WR + wr) * SB;
+    const int slot0 = blockIdx.x * SB;
     const int r0 = blockIdx.y * RB;
     const Slot mine = read_slot(p, lane < SB ? slot0 + lane : p.slots);
-    uint32_t starts = segment_starts(mine.adapter, lane, SB);
+    const uint32_t starts = segment_starts(mine.adapter, lane, SB);
     const int segs = __popc(starts);
-    const int ks_count = max(1, WK / segs); // k slices per segment
+    const int slices = max(1, LORA_WARPS / segs);
     const int k_lo = blockIdx.z * p.k_chunk, k_hi = min(k_lo + p.k_chunk, p.K);
-    const int k_step = ((k_hi - k_lo + ks_count - 1) / ks_count + 63) / 64 * 64;
-    float *my_red = red + (size_t)wr * WK * SB * RB;
+    const int k_step = ((k_hi - k_lo + slices - 1) / slices + 31) / 32 * 32;
 
-    for (int job = wk; job < segs * ks_count; job += WK) {
-        const int seg = job / ks_count, ks = job % ks_count;
+    for (int job = warp; job < segs * slices; job += LORA_WARPS) {
+        const int seg = job / slices, ks = job % slices;
         uint32_t left = starts;
         for (int i = 0; i < seg; ++i)
             left &= left - 1;
@@ -139,76 +138,70 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParam
         const int g = __shfl_sync(0xffffffffu, mine.adapter, s0);
         if (g < 0)
             continue;
-        const uint16_t *xrow[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = m * 16 + h * 8 + q;
-                const int row = __shfl_sync(0xffffffffu, mine.row, s);
-                xrow[m][h] = s >= s0 && s < s1 ? static_cast<const uint16_t *>(p.x) + (size_t)row * p.ld_x : nullptr;
-            }
-        const uint16_t *arow[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int r = r0 + 8 * j + q;
-            arow[j] = r < p.R ? static_cast<const uint16_t *>(p.lora_a) + ((size_t)g * p.R + r) * p.K : nullptr;
-        }
-        float acc[MT][NT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[m][j][e] = 0.0f;
+        // slots outside the segment and ranks past R read a row that is there:
+        // their products are not used
         const int ka = k_lo + ks * k_step, kb = min(ka + k_step, k_hi);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-        for (int k = ka; k < kb; k += 32) {
-            const int at = k + t * 8;
-            const bool in = at < kb;
-            uint4 xv[MT][2], av[NT];
+        const uint16_t *xrow[2], *arow[NT];
+        const int first_row = __shfl_sync(0xffffffffu, mine.row, s0);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    xv[m][h] = in && xrow[m][h] ? __ldg(reinterpret_cast<const uint4 *>(xrow[m][h] + at)) : zero;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                av[j] = in && arow[j] ? __ldg(reinterpret_cast<const uint4 *>(arow[j] + at)) : zero;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma_16816<BF16>(acc[m][j], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, av[j].x, av[j].y);
-                    mma_16816<BF16>(acc[m][j], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, av[j].z, av[j].w);
-                }
+        for (int h = 0; h < 2; ++h) {
+            const int s = h * 8 + q;
+            const int row = __shfl_sync(0xffffffffu, mine.row, s);
+            xrow[h] = static_cast<const uint16_t *>(p.x) + (size_t)(s >= s0 && s < s1 ? row : first_row) * p.ld_x +
+                      ka + t * 8;
         }
-        // each row of the segment, ks-th slice
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int j = 0; j < NT; ++j)
+            arow[j] = static_cast<const uint16_t *>(p.lora_a) + ((size_t)g * p.R + min(r0 + 8 * j + q, p.R - 1)) * p.K +
+                      ka + t * 8;
+        float acc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[j][e] = 0.0f;
+        auto step = [&](bool in) {
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            uint4 xv[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int s = m * 16 + h * 8 + q;
-                if (s >= s0 && s < s1) {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        *reinterpret_cast<float2 *>(my_red + ((size_t)ks * SB + s) * RB + 8 * j + 2 * t) =
-                            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-                }
+                xv[h] = in ? __ldg(reinterpret_cast<const uint4 *>(xrow[h])) : zero;
+                xrow[h] += 32;
             }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint4 av = in ? __ldg(reinterpret_cast<const uint4 *>(arow[j])) : zero;
+                arow[j] += 32;
+                mma_16816<BF16>(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av.x, av.y);
+                mma_16816<BF16>(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av.z, av.w);
+            }
+        };
+        int k = ka;
+#pragma unroll(NT >= 8 ? 2 : 4)
+        for (; k + 32 <= kb; k += 32)
+            step(true);
+        if (k < kb) // the end of K: a multiple of 8
+            step(k + t * 8 < kb);
+        // each slot of the segment, ks-th slice
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s = h * 8 + q;
+            if (s >= s0 && s < s1) {
+                float2 *to = reinterpret_cast<float2 *>(red) + ((ks * SB + s) * RB + 2 * t) / 2;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    to[4 * j] = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+            }
+        }
     }
     __syncthreads();
-    // sum the slices; the group's warps share its slots
-    const int gt = threadIdx.x - wr * WK * 32;
-    for (int i = gt; i < SB * (RB / 4); i += WK * 32) {
+    for (int i = threadIdx.x; i < SB * (RB / 4); i += LORA_THREADS) {
         const int s = i / (RB / 4), r = i % (RB / 4) * 4;
         if (slot0 + s >= p.slots || r0 + r >= p.R)
             continue;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int ks = 0; ks < ks_count; ++ks) {
-            const float4 v = *reinterpret_cast<const float4 *>(my_red + ((size_t)ks * SB + s) * RB + r);
+        for (int ks = 0; ks < slices; ++ks) {
+            const float4 v = red[((ks * SB + s) * RB + r) / 4];
             sum.x += v.x;
             sum.y += v.y;
             sum.z += v.z;
@@ -221,165 +214,184 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParam
 
 // ---------------------------------------------------------------- up
 
-// MT blocks of 16 slots per CTA (all its warps), `p.n_chunk` columns per CTA.
-template <bool BF16, int MT>
-__global__ void __launch_bounds__(LORA_THREADS) lora_up_kernel(const LoraParams p)
+// 8 slots and `p.n_chunk` columns per CTA.  A warp's job is 64 columns of one
+// segment, two per lane, 16 ranks at a time in FP32: with one or two rows per
+// adapter, as in a decode batch, that takes a third of the instructions of an
+// MMA with its 16 rows (13.5 -> NEW us for 64 rows of 28 adapters, N = 7168).
+template <bool BF16>
+__global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraParams p)
 {
-    constexpr int SB = 16 * MT;
-    extern __shared__ uint8_t smem[];
-    // v as two 16-bit terms, [SB][pitch] each; pitch: R rounded up to 16, plus
-    // 8 so that the 8 rows of a fragment load fall into distinct banks
-    const int pitch = (p.R + 15) / 16 * 16 + 8;
-    uint16_t *hi = reinterpret_cast<uint16_t *>(smem);
-    uint16_t *lo = hi + SB * pitch;
+    constexpr int SB = LORA_UP_SLOTS;
+    extern __shared__ float4 part[]; // [share][slot][rank / 4]
     __shared__ float row_scale[SB];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = lane & 3, q = lane >> 2;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    __shared__ int seg_first[SB + 1], seg_adapter[SB], slot_row[SB];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Everything but v is ready: the first kernel let this one start only
+    // after its own wait for the kernels before it.  So the slots and the
+    // first job's operands are read while the first kernel runs.
     const int slot0 = blockIdx.x * SB;
     const Slot mine = read_slot(p, lane < SB ? slot0 + lane : p.slots);
     const uint32_t starts = segment_starts(mine.adapter, lane, SB);
     const int segs = __popc(starts);
-
-    // v of the CTA's slots: each warp sums the ranges of its rows in order
-    for (int s = warp; s < SB; s += LORA_WARPS) {
-        const int g = __shfl_sync(0xffffffffu, mine.adapter, s);
-        if (g < 0)
-            continue;
-        const float *src = p.v + (size_t)(slot0 + s) * p.R;
-        const size_t step = (size_t)p.slots * p.R;
-        float scale = 1.0f;
-        float keep[8]; // R <= 256: lane + 32 i
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = lane + 32 * i;
-            float sum = 0.0f;
-            if (r < p.R) {
-#pragma unroll 8
-                for (int z = 0; z < p.splits; ++z)
-                    sum += __ldcg(src + z * step + r);
-            }
-            keep[i] = sum;
-            amax = fmaxf(amax, fabsf(sum));
-        }
-        if constexpr (!BF16) {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            // the largest value into [2^12, 2^13): both terms are normal
-            // numbers down to 2^-15 of it
-            if (amax > 0.0f && amax < __int_as_float(0x7f800000)) {
-                const int e = min(max(ilogbf(amax) - 12, -100), 115);
-                scale = ldexpf(1.0f, e);
-            }
-        }
-        const float inv = 1.0f / scale; // a power of two: exact
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = lane + 32 * i;
-            if (r < pitch - 8) {
-                const float v = keep[i] * inv; // 0 past R
-                const uint32_t h = pack2<BF16>(v, 0.0f);
-                const float top = unpack2<BF16>(h).x;
-                // an infinite or NaN v has no second term
-                const float rest = isfinite(top) ? v - top : 0.0f;
-                hi[s * pitch + r] = (uint16_t)h;
-                lo[s * pitch + r] = (uint16_t)pack2<BF16>(rest, 0.0f);
-            }
+    if (warp == 0 && lane < SB) {
+        if ((starts >> lane) & 1u) {
+            const int i = __popc(starts & ((1u << lane) - 1u));
+            seg_first[i] = lane;
+            seg_adapter[i] = mine.adapter;
         }
         if (lane == 0)
-            row_scale[s] = scale * __ldg(p.scales + g);
+            seg_first[segs] = SB;
+        slot_row[lane] = mine.row;
     }
     __syncthreads();
 
-    // jobs: 32 columns of one segment
     const int n_lo = blockIdx.y * p.n_chunk, n_hi = min(n_lo + p.n_chunk, p.N);
-    const int col_groups = (n_hi - n_lo + 31) / 32;
-    for (int job = warp; job < segs * col_groups; job += LORA_WARPS) {
-        const int seg = job % segs;
-        uint32_t left = starts;
-        for (int i = 0; i < seg; ++i)
-            left &= left - 1;
-        const int s0 = __ffs(left) - 1;
-        left &= left - 1;
-        const int s1 = left ? __ffs(left) - 1 : SB;
-        const int g = __shfl_sync(0xffffffffu, mine.adapter, s0);
+    // the job's B: ranks k0 to k0 + 15 of columns n and n + 1 (zero past R; a
+    // column pair past the end reads the last one's and is not stored)
+    uint4 b[2][2];
+    auto load_b = [&](int g, int n, int k0) {
+        const uint16_t *base =
+            static_cast<const uint16_t *>(p.lora_b) + ((long)g * p.N + min(n, n_hi - 2)) * p.R + k0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                b[c][h] = k0 + 8 * h < p.R ? __ldg(reinterpret_cast<const uint4 *>(base + (long)c * p.R) + h)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint32_t cv[SB];
+    auto load_c = [&](int s0, int s1, int n) {
+#pragma unroll
+        for (int s = 0; s < SB; ++s)
+            if (s >= s0 && s < s1 && n < n_hi)
+                cv[s] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.c) +
+                                                            (long)slot_row[s] * p.ld_c + n);
+    };
+    int seg = warp - LORA_WARPS, n0 = n_lo;
+    auto advance = [&]() { // to this warp's next job
+        seg += LORA_WARPS;
+        while (seg >= segs) {
+            seg -= segs;
+            n0 += 64;
+        }
+    };
+    auto load_job = [&]() {
+        const int g = seg_adapter[seg];
+        if (g >= 0) {
+            load_b(g, n0 + 2 * lane, 0);
+            load_c(seg_first[seg], seg_first[seg + 1], n0 + 2 * lane);
+        }
+    };
+    advance();
+    if (n0 < n_hi)
+        load_job();
+    if (warp == 0 && lane < SB) // read after the next barriers
+        row_scale[lane] = mine.adapter >= 0 ? __ldg(p.scales + mine.adapter) : 0.0f;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // v of the CTA's slots.  Thread: one float4 of ranks of one slot, a share
+    // of the k ranges if there are threads to spare; the shares are joined in
+    // order below.
+    const int r4 = p.R / 4;
+    const int items = min(SB, p.slots - slot0) * r4;
+    const int shares = max(1, min(p.splits, LORA_THREADS / items));
+    {
+        const int per = (p.splits + shares - 1) / shares;
+        const long step = (long)p.slots * r4;
+        const float4 *src = reinterpret_cast<const float4 *>(p.v) + (long)slot0 * r4;
+        for (int i = tid; i < items * shares; i += LORA_THREADS) {
+            const int item = i % items, z0 = i / items * per, z1 = min(z0 + per, p.splits);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int z = z0; z < z1; ++z) {
+                const float4 v = __ldcg(src + z * step + item);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            part[i] = sum;
+        }
+    }
+    __syncthreads();
+    if (shares > 1) {
+        // (then there are at most LORA_THREADS items, one per thread)
+        if (tid < items) {
+            float4 sum = part[tid];
+            for (int z = 1; z < shares; ++z) {
+                const float4 v = part[z * items + tid];
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            part[tid] = sum;
+        }
+        __syncthreads();
+    }
+
+    bool loaded = true;
+    for (; n0 < n_hi; advance(), loaded = false) {
+        const int g = seg_adapter[seg];
         if (g < 0)
             continue;
-        const int n0 = n_lo + job / segs * 32;
-        // MMA column c of block j is column n0 + (c / 2) * 8 + 2 j + c % 2, so
-        // that a lane's results are 8 consecutive columns
-        const uint16_t *brow[4];
+        if (!loaded)
+            load_job();
+        const int s0 = seg_first[seg], s1 = seg_first[seg + 1];
+        const int n = n0 + 2 * lane;
+        float acc[SB][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + (q >> 1) * 8 + 2 * j + (q & 1);
-            brow[j] = n < n_hi ? static_cast<const uint16_t *>(p.lora_b) + ((size_t)g * p.N + n) * p.R : nullptr;
-        }
-        const int col = n0 + t * 8;
-        const bool col_ok = col < n_hi;
-        float acc[MT][4][4];
-        uint4 cv[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int s = 0; s < SB; ++s)
+            acc[s][0] = acc[s][1] = 0.0f;
+        for (int k0 = 0; k0 < p.R; k0 += 16) {
+            if (k0 > 0)
+                load_b(g, n, k0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int s = m * 16 + h * 8 + q;
-                const int row = __shfl_sync(0xffffffffu, mine.row, s);
-                if (s >= s0 && s < s1 && col_ok)
-                    cv[m][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.c) +
-                                                                (size_t)row * p.ld_c + col);
-            }
+                float w[2][8];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t raw[4] = {b[c][h].x, b[c][h].y, b[c][h].z, b[c][h].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[m][j][e] = 0.0f;
-#pragma unroll 2
-        for (int k = 0; k < p.R; k += 16) {
-            const int at = k + t * 4;
-            uint2 b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                b[j] = brow[j] && at < p.R ? __ldg(reinterpret_cast<const uint2 *>(brow[j] + at)) : make_uint2(0u, 0u);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m * 16 >= s1 || m * 16 + 16 <= s0)
-                    continue;
-                const uint16_t *h0 = hi + (m * 16 + q) * pitch + at, *l0 = lo + (m * 16 + q) * pitch + at;
-                const uint2 ha = *reinterpret_cast<const uint2 *>(h0);
-                const uint2 hb = *reinterpret_cast<const uint2 *>(h0 + 8 * pitch);
-                const uint2 la = *reinterpret_cast<const uint2 *>(l0);
-                const uint2 lb = *reinterpret_cast<const uint2 *>(l0 + 8 * pitch);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma_16816<BF16>(acc[m][j], ha.x, hb.x, ha.y, hb.y, b[j].x, b[j].y);
-                    mma_16816<BF16>(acc[m][j], la.x, lb.x, la.y, lb.y, b[j].x, b[j].y);
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = m * 16 + h * 8 + q;
-                const int row = __shfl_sync(0xffffffffu, mine.row, s);
-                if (s >= s0 && s < s1 && col_ok) {
-                    const float f = row_scale[s];
-                    const uint32_t in[4] = {cv[m][h].x, cv[m][h].y, cv[m][h].z, cv[m][h].w};
-                    uint32_t out[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 old = unpack2<BF16>(in[j]);
-                        out[j] = pack2<BF16>(fmaf(f, acc[m][j][2 * h], old.x), fmaf(f, acc[m][j][2 * h + 1], old.y));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack2<BF16>(raw[i]);
+                        w[c][2 * i] = f.x;
+                        w[c][2 * i + 1] = f.y;
                     }
-                    st_global_v4(static_cast<uint16_t *>(p.d) + (size_t)row * p.ld_d + col, out[0], out[1], out[2],
-                                 out[3]);
+                }
+                if (k0 + 8 * h >= p.R) // past R: neither v nor B
+                    break;
+#pragma unroll
+                for (int s = 0; s < SB; ++s) {
+                    if (s < s0 || s >= s1)
+                        continue;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 v = part[s * r4 + (k0 + 8 * h) / 4 + i];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            acc[s][c] = fmaf(v.x, w[c][4 * i], acc[s][c]);
+                            acc[s][c] = fmaf(v.y, w[c][4 * i + 1], acc[s][c]);
+                            acc[s][c] = fmaf(v.z, w[c][4 * i + 2], acc[s][c]);
+                            acc[s][c] = fmaf(v.w, w[c][4 * i + 3], acc[s][c]);
+                        }
+                    }
                 }
             }
+        }
+        if (n < n_hi) {
+#pragma unroll
+            for (int s = 0; s < SB; ++s) {
+                if (s < s0 || s >= s1)
+                    continue;
+                const float2 old = unpack2<BF16>(cv[s]);
+                const float f = row_scale[s];
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.d) + (long)slot_row[s] * p.ld_d + n) =
+                    pack2<BF16>(fmaf(f, acc[s][0], old.x), fmaf(f, acc[s][1], old.y));
+            }
+        }
     }
 }
 
@@ -398,82 +410,59 @@ cudaError_t launch_pdl(void (*kernel)(LoraParams), dim3 grid, size_t smem, const
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool BF16, int MT, int NT, int WR>
-cudaError_t down(const LoraParams &p, const LoraPlan &plan, cudaStream_t stream)
+template <bool BF16, int NT>
+cudaError_t down(const LoraParams &p, cudaStream_t stream)
 {
-    constexpr size_t smem = sizeof(float) * LORA_WARPS * 16 * MT * 8 * NT;
-    static std::atomic<bool> ready[64];
-    auto kernel = lora_down_kernel<BF16, MT, NT, WR>;
-    if (smem > 48 * 1024 && !ready[plan.device].load(std::memory_order_acquire)) {
-        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (err != cudaSuccess)
-            return err;
-        ready[plan.device].store(true, std::memory_order_release);
-    }
-    const int slots_per_cta = 16 * MT * WR;
-    const dim3 grid((unsigned)((p.slots + slots_per_cta - 1) / slots_per_cta), (unsigned)((p.R + 8 * NT - 1) / (8 * NT)),
+    const dim3 grid((unsigned)((p.slots + LORA_SLOTS - 1) / LORA_SLOTS), (unsigned)((p.R + 8 * NT - 1) / (8 * NT)),
                     (unsigned)p.splits);
-    return launch_pdl(kernel, grid, smem, p, stream);
-}
-
-template <bool BF16, int MT, int WR>
-cudaError_t down_rank(const LoraParams &p, const LoraPlan &plan, cudaStream_t stream)
-{
-    if (p.R <= 16)
-        return down<BF16, MT, 2, WR>(p, plan, stream);
-    if (p.R <= 32)
-        return down<BF16, MT, 4, WR>(p, plan, stream);
-    return down<BF16, MT, 8, WR>(p, plan, stream);
-}
-
-template <bool BF16, int MT>
-cudaError_t up(const LoraParams &p, const LoraPlan &plan, cudaStream_t stream)
-{
-    const size_t smem = sizeof(uint16_t) * 2 * 16 * MT * ((p.R + 15) / 16 * 16 + 8);
-    const dim3 grid((unsigned)((p.slots + 16 * MT - 1) / (16 * MT)), (unsigned)((p.N + p.n_chunk - 1) / p.n_chunk), 1);
-    return launch_pdl(lora_up_kernel<BF16, MT>, grid, smem, p, stream);
+    return launch_pdl(lora_down_kernel<BF16, NT>, grid, 0, p, stream);
 }
 
 template <bool BF16>
-cudaError_t both(const LoraParams &p, const LoraPlan &plan, cudaStream_t stream)
+cudaError_t up(const LoraParams &p, cudaStream_t stream)
 {
-    cudaError_t err = plan.wide ? down_rank<BF16, 2, 4>(p, plan, stream) : down_rank<BF16, 1, 1>(p, plan, stream);
+    const size_t sums = sizeof(float) * LORA_UP_SLOTS * p.R, threads = sizeof(float4) * LORA_THREADS;
+    const dim3 grid((unsigned)((p.slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS),
+                    (unsigned)((p.N + p.n_chunk - 1) / p.n_chunk), 1);
+    return launch_pdl(lora_up_kernel<BF16>, grid, sums > threads ? sums : threads, p, stream);
+}
+
+template <bool BF16>
+cudaError_t both(const LoraParams &p, cudaStream_t stream)
+{
+    const cudaError_t err = p.R <= 16 ? down<BF16, 2>(p, stream)
+                          : p.R <= 32 ? down<BF16, 4>(p, stream) : down<BF16, 8>(p, stream);
     if (err != cudaSuccess)
         return err;
-    return plan.wide ? up<BF16, 2>(p, plan, stream) : up<BF16, 1>(p, plan, stream);
+    return up<BF16>(p, stream);
 }
 
 } // namespace
 
-// How a call is cut up, from its sizes alone (the workspace follows from it).
-// Few slots: 16 per CTA and all 8 warps on one k range; many: 128 per CTA, 32
-// per warp.  The k ranges and the column chunks are cut so that either kernel
-// has about two CTAs per SM.
+// How a call is cut up, from its sizes alone (the workspace follows from it):
+// k ranges and column chunks so that either kernel has about four CTAs per SM,
+// at most 32 ranges (which the second kernel adds up in one or two rounds of
+// loads), at least 64 wide.
 LoraPlan lora_plan(int slots, int R, int N, int K)
 {
     LoraPlan plan = {};
-    slots = slots > 0 ? slots : 1;
-    plan.wide = slots > 256;
-    const int sms = 148;
-    const long down_blocks = (long)((slots + (plan.wide ? 127 : 15)) / (plan.wide ? 128 : 16)) *
-                             ((R + 63) / 64);
-    const int unit = plan.wide ? 128 : 256; // k of one pass of a CTA's warps
-    long splits = (2 * sms + down_blocks - 1) / down_blocks;
-    const long most = (K + unit - 1) / unit;
+    const long ctas = 4 * 148;
+    const long blocks = slots > 0 ? ((long)slots + LORA_SLOTS - 1) / LORA_SLOTS : 1;
+    const long down_blocks = blocks * ((R + 63) / 64);
+    long splits = ctas / down_blocks;
+    const long most = (K + 63) / 64 < 32 ? (K + 63) / 64 : 32;
     splits = splits < 1 ? 1 : splits > most ? most : splits;
-    plan.k_chunk = (int)((K + splits * unit - 1) / (splits * unit) * unit);
+    plan.k_chunk = (int)((K + splits * 64 - 1) / (splits * 64) * 64);
     plan.splits = (K + plan.k_chunk - 1) / plan.k_chunk;
-    const long up_blocks = (slots + (plan.wide ? 31 : 15)) / (plan.wide ? 32 : 16);
-    long chunks = (3 * sms + up_blocks - 1) / up_blocks;
-    const long most_chunks = (N + 127) / 128;
-    chunks = chunks < 1 ? 1 : chunks > most_chunks ? most_chunks : chunks;
-    plan.n_chunk = (int)((N + chunks * 128 - 1) / (chunks * 128) * 128);
+    const long up_blocks = slots > 0 ? ((long)slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS : 1;
+    const long chunk = ((long)N * up_blocks + ctas - 1) / ctas;
+    plan.n_chunk = (int)((chunk < N ? chunk : N) + 63) / 64 * 64;
     return plan;
 }
 
-cudaError_t launch_lora(const LoraParams &p, const LoraPlan &plan, bool bf16, cudaStream_t stream)
+cudaError_t launch_lora(const LoraParams &p, bool bf16, cudaStream_t stream)
 {
-    return bf16 ? both<true>(p, plan, stream) : both<false>(p, plan, stream);
+    return bf16 ? both<true>(p, stream) : both<false>(p, stream);
 }
 
 } // namespace fp8nt
