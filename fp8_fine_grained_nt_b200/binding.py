@@ -10,6 +10,7 @@ fails to load, the call raises (there is no fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -121,7 +122,7 @@ def load_library():
         lib.get_group_rows_workspace_size.restype = L
         lib.m_grouped_lora_add.argtypes = [P, L, P, P, P, P, L, P, L, P, P, I, I, I, I, I, I, I, P,
                                            Z, P]
-        lib.get_lora_workspace_size.argtypes = [I, I, I, I]
+        lib.get_lora_workspace_size.argtypes = [I, I, I, I, I]
         lib.get_lora_workspace_size.restype = L
         lib.dg_force_ragged.argtypes = [I, I, I]
         _lib = lib
@@ -264,40 +265,63 @@ def m_grouped_gemm_fp8_fp8_bf16_nt_masked(a, sa, b, sb, d, masked_m, expected_m:
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _HALF = (torch.bfloat16, torch.float16)
-_I32 = (torch.int32,)
 
 
-def _call(name: str, stream, device: torch.device, *args) -> None:
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device that `t` is on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _arg(t: torch.Tensor, name: str, dtype, ndim: int, device: int, dense: bool = True) -> int:
+    """Checked pointer of a tensor on `device` (`dense`: contiguous; else only its rows are)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}, not on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    if not t.is_contiguous() and (dense or (t.size(1) > 1 and t.stride(1) != 1)):
+        raise ValueError(f"{name} must be contiguous" if dense else f"{name} must have contiguous rows")
+    return t.data_ptr()
+
+
+def _half(t: torch.Tensor, name: str):
+    """The 16-bit type of a call, from its first operand."""
+    if t.dtype not in _HALF:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_HALF}")
+    return t.dtype
+
+
+def _call(name: str, stream, device: int, *args) -> None:
     """Call the library on the tensors' own device, on `stream` or that device's current one."""
-    lib = _lib or load_library()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    fn = getattr(lib, name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{device}")
+    else:
+        raw = stream.cuda_stream
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == device:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, raw)
     if status != 0:
         raise Fp8NtError(status, name)
 
 
-def _same_device(*tensors: torch.Tensor) -> torch.device:
-    device = tensors[0].device
-    for t in tensors:
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    return device
-
-
 def _ragged(name: str, a, b, d, offsets, G: int, N: int, K: int, stream):
-    dtypes = (a.dtype,) if a.dtype in _HALF else _HALF
-    args = (_dev(a, "a", dtypes, 2), _dev(b, "b", dtypes, 3), _dev(d, "d", dtypes, 2),
-            _dev(offsets, "offsets", _I32, 1))
-    _call(name, stream, _same_device(a, b, d, offsets), *args, _DTYPE_CODE[a.dtype], G, a.shape[0],
-          N, K)
+    device, dtype = _device_of(a, "a"), _half(a, "a")
+    _call(name, stream, device, _arg(a, "a", dtype, 2, device), _arg(b, "b", dtype, 3, device),
+          _arg(d, "d", dtype, 2, device), _arg(offsets, "offsets", torch.int32, 1, device),
+          _DTYPE_CODE[dtype], G, a.size(0), N, K)
     return d
 
 
@@ -340,32 +364,33 @@ def k_grouped_gemm_tn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
     G, N, K = d.shape
     if a.shape[1] != N or b.shape[1] != K or a.shape[0] != b.shape[0] or offsets.shape[0] != G + 1:
         raise ValueError("shape mismatch between a, b, d and offsets")
-    dtypes = (a.dtype,) if a.dtype in _HALF else _HALF
-    args = (_dev(a, "a", dtypes, 2), _dev(b, "b", dtypes, 2),
-            _dev(d, "d", dtypes if not accumulate else _F32, 3) if d.dtype != torch.float32
-            else _dev(d, "d", _F32, 3), _dev(offsets, "offsets", _I32, 1))
-    _call("k_grouped_gemm_tn_ragged", stream, _same_device(a, b, d, offsets), *args,
-          _DTYPE_CODE[a.dtype], _DTYPE_CODE[d.dtype], int(accumulate), G, a.shape[0], N, K)
+    device, dtype = _device_of(a, "a"), _half(a, "a")
+    d_dtype = torch.float32 if accumulate or d.dtype is torch.float32 else dtype
+    _call("k_grouped_gemm_tn_ragged", stream, device, _arg(a, "a", dtype, 2, device),
+          _arg(b, "b", dtype, 2, device), _arg(d, "d", d_dtype, 3, device),
+          _arg(offsets, "offsets", torch.int32, 1, device), _DTYPE_CODE[dtype], _DTYPE_CODE[d_dtype],
+          int(accumulate), G, a.size(0), N, K)
     return d
 
 
-def _workspace(given, need: int, stream, device: torch.device):
+def _workspace(given, need: int, stream, device: int):
     """(pointer, bytes, owner) of the caller's workspace, or of one from torch's
     allocator that belongs to the stream the call runs on."""
     if given is not None:
-        if given.device != device or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if given.get_device() != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
         return given.data_ptr(), given.numel() * given.element_size(), given
     if need == 0:
         return 0, 0, None
     if stream is None:
-        own = torch.empty(need, dtype=torch.uint8, device=device)
+        own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
     else:
         with torch.cuda.stream(stream):
-            own = torch.empty(need, dtype=torch.uint8, device=device)
+            own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
     return own.data_ptr(), need, own
 
 
+@functools.lru_cache(maxsize=4096)
 def _size(name: str, *args: int) -> int:
     n = getattr(_lib or load_library(), name)(*args)
     if n < 0:
@@ -396,41 +421,26 @@ def group_rows_by_index(index: torch.Tensor, num_groups: int, offsets: torch.Ten
     -1 (optional); capacity = get_row_groups_capacity(R, num_groups, alignment).
     Returns (offsets, order, slots, m_indices).
     """
-    R = index.shape[0]
-    cap = get_row_groups_capacity(R, num_groups, alignment)
-    args = (_dev(index, "index", (torch.int32, torch.int64), 1), 1 if index.dtype == torch.int64 else 0,
-            _dev(offsets, "offsets", _I32, 1), _dev(order, "order", _I32, 1),
-            None if slots is None else _dev(slots, "slots", _I32, 1),
-            None if m_indices is None else _dev(m_indices, "m_indices", _I32, 1))
-    if (offsets.shape[0] != num_groups + 1 or order.shape[0] != cap
-            or (slots is not None and slots.shape[0] != R)
-            or (m_indices is not None and m_indices.shape[0] != cap)):
+    device = _device_of(index, "index")
+    if index.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"index has dtype {index.dtype}, expected int32 or int64")
+    args = (_arg(index, "index", index.dtype, 1, device), 1 if index.dtype is torch.int64 else 0,
+            _arg(offsets, "offsets", torch.int32, 1, device), _arg(order, "order", torch.int32, 1, device),
+            None if slots is None else _arg(slots, "slots", torch.int32, 1, device),
+            None if m_indices is None else _arg(m_indices, "m_indices", torch.int32, 1, device))
+    R = index.size(0)
+    cap = _size("get_row_groups_capacity", R, num_groups, alignment)
+    if (offsets.size(0) != num_groups + 1 or order.size(0) != cap or (slots is not None and slots.size(0) != R)
+            or (m_indices is not None and m_indices.size(0) != cap)):
         raise ValueError(f"offsets must hold {num_groups + 1} values, order and m_indices {cap}, slots {R}")
-    device = _same_device(*(t for t in (index, offsets, order, slots, m_indices) if t is not None))
-    ptr, size, _own = _workspace(workspace, get_group_rows_workspace_size(R, num_groups), stream, device)
+    ptr, size, _own = _workspace(workspace, _size("get_group_rows_workspace_size", R, num_groups), stream, device)
     _call("group_rows_by_index", stream, device, *args, R, num_groups, alignment, ptr, size)
     return offsets, order, slots, m_indices
 
 
-def get_lora_workspace_size(num_slots: int, rank: int, N: int, K: int) -> int:
-    """Bytes of workspace m_grouped_lora_add needs."""
-    return _size("get_lora_workspace_size", int(num_slots), int(rank), int(N), int(K))
-
-
-def _rows(t: torch.Tensor, name: str, dtypes) -> tuple[int, int]:
-    """(pointer, row stride) of a 2-D tensor whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+def get_lora_workspace_size(num_slots: int, num_adapters: int, rank: int, N: int, K: int) -> int:
+    """Bytes of workspace m_grouped_lora_add needs (0 for long batches)."""
+    return _size("get_lora_workspace_size", int(num_slots), int(num_adapters), int(rank), int(N), int(K))
 
 
 def m_grouped_lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
@@ -448,21 +458,23 @@ def m_grouped_lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tens
     (group_rows_by_index) share the reads of its weights.
     """
     L, R, K = lora_a.shape
-    (T, N), S = d.shape, m_indices.shape[0]
-    if (x.shape[0] != T or x.shape[1] != K or tuple(lora_b.shape) != (L, N, R) or tuple(c.shape) != (T, N)
-            or scales.shape[0] != L or (order is not None and order.shape[0] != S)):
+    T, N = d.shape
+    S = m_indices.size(0)
+    if (x.shape != (T, K) or lora_b.shape != (L, N, R) or c.shape != (T, N) or scales.size(0) != L
+            or (order is not None and order.size(0) != S)):
         raise ValueError("shape mismatch between x, lora_a, lora_b, scales, c, d, m_indices and order")
     if order is None and S > T:
         raise ValueError(f"m_indices holds {S} slots for {T} rows")
-    dtypes = (x.dtype,) if x.dtype in _HALF else _HALF
-    args = (*_rows(x, "x", dtypes), _dev(lora_a, "lora_a", dtypes, 3), _dev(lora_b, "lora_b", dtypes, 3),
-            _dev(scales, "scales", _F32, 1), *_rows(c, "c", dtypes), *_rows(d, "d", dtypes),
-            _dev(m_indices, "m_indices", _I32, 1), None if order is None else _dev(order, "order", _I32, 1))
-    device = _same_device(x, lora_a, lora_b, scales, c, d, m_indices)
-    if order is not None:
-        _same_device(x, order)
-    ptr, size, _own = _workspace(workspace, get_lora_workspace_size(S, R, N, K), stream, device)
-    _call("m_grouped_lora_add", stream, device, *args, _DTYPE_CODE[x.dtype], S, T, L, R, N, K, ptr, size)
+    device, dtype = _device_of(x, "x"), _half(x, "x")
+    args = (_arg(x, "x", dtype, 2, device, False), x.stride(0) if T > 1 else K,
+            _arg(lora_a, "lora_a", dtype, 3, device), _arg(lora_b, "lora_b", dtype, 3, device),
+            _arg(scales, "scales", torch.float32, 1, device),
+            _arg(c, "c", dtype, 2, device, False), c.stride(0) if T > 1 else N,
+            _arg(d, "d", dtype, 2, device, False), d.stride(0) if T > 1 else N,
+            _arg(m_indices, "m_indices", torch.int32, 1, device),
+            None if order is None else _arg(order, "order", torch.int32, 1, device))
+    ptr, size, _own = _workspace(workspace, _size("get_lora_workspace_size", S, L, R, N, K), stream, device)
+    _call("m_grouped_lora_add", stream, device, *args, _DTYPE_CODE[dtype], S, T, L, R, N, K, ptr, size)
     return d
 
 

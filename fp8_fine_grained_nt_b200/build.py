@@ -144,7 +144,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         return LIB_PATH
     jobs = jobs or max(1, os.cpu_count() or 1)
     tasks = [(os.path.join(CSRC, f"{name}.cu"), os.path.join(BUILD_DIR, f"{name}.o"), [], name)
-             for name in ("api", "api_grouped", "group_rows", "lora", "quantize", "selftest")]
+             for name in ("api", "api_grouped", "group_rows", "lora", "lora_wide", "quantize", "selftest")]
     for mw, bn, pair, scalar in kernel_list():
         tag = f"mw{mw}_bn{bn}_p{pair}_s{scalar}"
         tasks.append((os.path.join(CSRC, "instance.cu"), os.path.join(BUILD_DIR, f"kernel_{tag}.o"),

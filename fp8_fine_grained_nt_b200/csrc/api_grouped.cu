@@ -300,13 +300,15 @@ int group_rows_by_index(const void *index, int index_dtype, int *offsets, int *o
                : DG_ERR_CUDA;
 }
 
-long long get_lora_workspace_size(int num_slots, int rank, int N, int K)
+long long get_lora_workspace_size(int num_slots, int num_adapters, int rank, int N, int K)
 {
-    if (num_slots < 0 || rank < 0 || N < 0 || K < 0)
+    if (num_slots < 0 || num_adapters <= 0 || rank < 0 || N < 0 || K < 0)
         return -DG_ERR_INVALID_ARGUMENT;
     if (num_slots > kMaxSlots || rank == 0 || rank > LORA_MAX_RANK || rank % 8 != 0 || N == 0 || N % 8 != 0 || K == 0 ||
         K % 8 != 0)
         return -DG_ERR_UNSUPPORTED_SHAPE;
+    if (num_slots == 0 || lora_is_wide(num_slots, num_adapters, rank))
+        return 0;
     return (long long)lora_plan(num_slots, rank, N, K).splits * num_slots * rank * 4;
 }
 
@@ -315,9 +317,9 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
                        int dtype, int num_slots, int num_rows, int num_adapters, int rank, int N, int K,
                        void *workspace, size_t workspace_bytes, dg_stream_t stream)
 {
-    if ((dtype != DG_INPUT_BF16 && dtype != DG_INPUT_F16) || num_rows < 0 || num_adapters <= 0)
+    if ((dtype != DG_INPUT_BF16 && dtype != DG_INPUT_F16) || num_rows < 0)
         return DG_ERR_INVALID_ARGUMENT;
-    const long long need = get_lora_workspace_size(num_slots, rank, N, K);
+    const long long need = get_lora_workspace_size(num_slots, num_adapters, rank, N, K);
     if (need < 0)
         return (int)-need;
     if (ld_x < K || ld_c < N || ld_d < N)
@@ -326,7 +328,7 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
         return DG_ERR_UNSUPPORTED_SHAPE;
     if (num_slots == 0 || num_rows == 0)
         return DG_OK;
-    if (!x || !lora_a || !lora_b || !scales || !c || !d || !m_indices || !workspace ||
+    if (!x || !lora_a || !lora_b || !scales || !c || !d || !m_indices || (need > 0 && !workspace) ||
         (long long)workspace_bytes < need)
         return DG_ERR_INVALID_ARGUMENT;
     if (!aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(c, 16) || !aligned(d, 16) ||
@@ -336,7 +338,6 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
     const int st = current_device(&dev);
     if (st != DG_OK)
         return st;
-    const LoraPlan plan = lora_plan(num_slots, rank, N, K);
     LoraParams p;
     memset(&p, 0, sizeof(p));
     p.x = x;
@@ -358,6 +359,9 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
     p.R = rank;
     p.N = N;
     p.K = K;
+    if (lora_is_wide(num_slots, num_adapters, rank))
+        return launch_lora_wide(p, dtype == DG_INPUT_BF16, dev, reinterpret_cast<cudaStream_t>(stream));
+    const LoraPlan plan = lora_plan(num_slots, rank, N, K);
     p.k_chunk = plan.k_chunk;
     p.splits = plan.splits;
     p.n_chunk = plan.n_chunk;

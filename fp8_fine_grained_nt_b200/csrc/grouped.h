@@ -50,7 +50,8 @@ cudaError_t launch_group_rows(const void *index, bool i64, int rows, int groups,
                               int *offsets, int *order, int *slots, int *m_indices, int *counts, unsigned int *status,
                               int device, cudaStream_t stream);
 
-// Low-rank adapters (csrc/lora.cu).
+// Low-rank adapters: few slots (csrc/lora.cu) and long batches
+// (csrc/lora_wide.cu).
 constexpr int LORA_MAX_RANK = 256;
 
 struct LoraParams {
@@ -76,5 +77,8 @@ struct LoraPlan {
 
 LoraPlan lora_plan(int slots, int R, int N, int K);
 cudaError_t launch_lora(const LoraParams &p, bool bf16, cudaStream_t stream);
+
+bool lora_is_wide(int slots, int adapters, int R);
+int launch_lora_wide(const LoraParams &p, bool bf16, const DeviceView &dev, cudaStream_t stream); // a dg_status
 
 } // namespace fp8nt

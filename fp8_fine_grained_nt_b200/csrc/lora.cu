@@ -26,7 +26,7 @@
 #include <atomic>
 
 #include "grouped.h"
-#include "ptx.cuh"
+#include "lora_common.cuh"
 
 namespace fp8nt {
 
@@ -52,48 +52,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    if constexpr (BF16)
-        return pack_bf16x2(lo, hi);
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w)
-{
-    if constexpr (BF16)
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
-// A slot's row and adapter, -1 where it has none (or a bad one, flagged).
-struct Slot {
-    int row;
-    int adapter;
-};
-
-__device__ __forceinline__ Slot read_slot(const LoraParams &p, int i)
-{
-    Slot s = {-1, -1};
-    if (i < p.slots) {
-        const int g = __ldg(p.m_indices + i);
-        const int t = p.order ? __ldg(p.order + i) : i;
-        if (g >= 0 && t >= 0) {
-            if (g < p.adapters && t < p.rows) {
-                s.row = t;
-                s.adapter = g;
-            } else {
-                atomicOr(p.status, DEVERR_BAD_INDEX);
-            }
-        }
-    }
-    return s;
 }
 
 // Bit i: a segment (run of one adapter) begins at slot i of a warp's slots, one

@@ -1,0 +1,705 @@
+// Low-rank adapters of many requests, long batches: both products on the
+// tensor cores in one kernel.
+//
+//   d[t, n] = c[t, n] + scale_g * sum_r v[t, r] B_g[n, r],   v[t, r] = sum_k x[t, k] A_g[r, k]
+//
+// A cluster of 1, 2, 4 or 8 CTAs takes 128 slots.  x, c and d are by far most
+// of the bytes, so each is touched once: every CTA of the cluster reads a
+// share of k of the slots' rows of x (v in FP32 in tensor memory), the shares
+// are added up in order through distributed shared memory, and every CTA adds
+// v B^T to a share of the columns.  v never leaves the SMs, and nothing needs
+// a workspace.
+//
+//   phase 1   four warps gather the slots' rows of x into a ring (cp.async,
+//             written in the layout the MMA reads), TMA brings A; M = 128
+//             slots, N = rank, 128 of k per stage.
+//   exchange  each CTA puts its FP32 share of v into its shared memory; after
+//             a cluster barrier every CTA adds the shares of its part of the
+//             slots in rank order, splits v into two 16-bit terms and writes
+//             them into every CTA's shared memory (hi + lo: 16 bits of
+//             mantissa with BF16, 22 with FP16, so that the middle result
+//             costs no accuracy; an FP16 row is divided by a power of two
+//             first, so that v may exceed its range).
+//   phase 2   128 columns at a time, hi B^T + lo B^T into one of two
+//             accumulators; the epilogue adds c, which it fetched into shared
+//             memory while the MMAs ran, rounds once and stores whole lines.
+//
+// Slots of more than one adapter: a pass over x handles four of them (one for
+// ranks above 64) with their own accumulators; a slot's lane picks its own, so
+// an adapter's Inf or NaN stays in its rows.  Slots sorted by adapter need one
+// pass almost everywhere.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "fp8_nt.h"
+#include "grouped.h"
+#include "kernel.cuh"
+#include "lora_common.cuh"
+
+namespace fp8nt {
+
+namespace {
+
+constexpr int WIDE_SLOTS = 128;
+constexpr int WIDE_THREADS = 512;
+constexpr int WIDE_WARPS = WIDE_THREADS / 32;
+constexpr int WIDE_MAX_STAGES = 8;
+constexpr int WIDE_BK = 128;                        // k per stage: two 64-wide swizzled halves
+constexpr uint32_t WIDE_X_BYTES = WIDE_SLOTS * 128; // 128 rows of 64 elements
+constexpr uint32_t WIDE_B_BYTES = 128 * 128;        // 128 columns x 64 ranks
+constexpr uint32_t WIDE_C_BYTES = WIDE_SLOTS * 256; // 128 slots x 128 columns
+
+struct WidePlan {
+    int cluster;
+    int segs;        // adapters per pass
+    int stages2;
+    uint32_t a_bytes; // 64 of k of one adapter's A
+    uint32_t ring;    // bytes of the first ring: as many stages as a pass's adapters allow
+    uint32_t off_c;     // two c buffers in the region of the first ring: behind the exchanged shares, or in their place
+    uint32_t off_v;     // hi, lo: [2][rank chunk][128][128 B]
+    uint32_t off_b;     // B ring
+    uint32_t off_bars;
+    uint32_t total;
+};
+
+struct WideParams {
+    LoraParams p;
+    WidePlan plan;
+    uint32_t idesc1, idesc2;
+    uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool in)
+{
+    // (a source size of 0 fills the 16 bytes with zeros)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Bit i: one of the warp's slots belongs to adapter i of the pass.
+__device__ __forceinline__ uint32_t segments_present(int mine, int segs)
+{
+    return __reduce_or_sync(0xffffffffu, mine >= 0 && mine < segs ? 1u << mine : 0u);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+    lora_wide_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const __grid_constant__ WideParams wp)
+{
+    const LoraParams &p = wp.p;
+    const WidePlan &plan = wp.plan;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *full1 = reinterpret_cast<uint64_t *>(smem + plan.off_bars); // x and A of a stage are there
+    uint64_t *empty1 = full1 + WIDE_MAX_STAGES;
+    uint64_t *full2 = empty1 + WIDE_MAX_STAGES; // B of a stage is there
+    uint64_t *empty2 = full2 + WIDE_MAX_STAGES;
+    uint64_t *p1_done = empty2 + WIDE_MAX_STAGES; // this CTA's share of v is complete
+    uint64_t *acc_full = p1_done + 1;             // accumulator complete (x2)
+    uint64_t *acc_empty = acc_full + 2;           // accumulator read (x2)
+    uint64_t *mma_done = acc_empty + 2;
+    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t abort_word;
+    __shared__ int slot_row[WIDE_SLOTS], slot_seg[WIDE_SLOTS]; // row; segment, -1 without an adapter
+    __shared__ int seg_adapter[WIDE_SLOTS];
+    __shared__ uint32_t warp_starts[4]; // slots of 32 at which a segment starts
+    __shared__ float adapter_scale[WIDE_SLOTS], slot_scale[WIDE_SLOTS]; // scale_g; times the power of two
+    volatile uint32_t *abort_flag = &abort_word;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        const uint32_t a = smem_addr(bar);
+        return mbar_try_wait(a, parity) || wait_slow(a, parity, abort_flag, p.status, wp.timeout_ns, true);
+    };
+
+    // ---------------------------------------------------------------- set-up
+    if (tid == 0) {
+        for (int s = 0; s < WIDE_MAX_STAGES; ++s) {
+            mbar_init(&full1[s], 4 + 1); // the gathering warps and the TMA thread
+            mbar_init(&empty1[s], 1);
+            mbar_init(&full2[s], 1);
+            mbar_init(&empty2[s], 1);
+        }
+        mbar_init(p1_done, 1);
+        mbar_init(mma_done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        abort_word = 0u;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmap_a);
+        tma_prefetch_desc(&tmap_b);
+    }
+    if (warp == 4) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int slot0 = blockIdx.y * WIDE_SLOTS;
+    // the block's slots and their segments (runs of one adapter)
+    Slot mine = {-1, -1};
+    if (warp < 4) {
+        mine = read_slot(p, slot0 + tid);
+        slot_row[tid] = mine.row;
+        slot_seg[tid] = mine.adapter;
+    }
+    __syncthreads();
+    const bool starts = warp < 4 && mine.adapter >= 0 && (tid == 0 || slot_seg[tid - 1] != mine.adapter);
+    const uint32_t start_mask = __ballot_sync(0xffffffffu, starts);
+    if (warp < 4 && lane == 0)
+        warp_starts[warp] = start_mask;
+    __syncthreads();
+    if (warp < 4) {
+        int seg = __popc(start_mask & (0xffffffffu >> (31 - lane))) - 1;
+        for (int w = 0; w < warp; ++w)
+            seg += __popc(warp_starts[w]);
+        slot_seg[tid] = mine.adapter >= 0 ? seg : -1;
+        if (starts)
+            seg_adapter[seg] = mine.adapter;
+        adapter_scale[tid] = mine.adapter >= 0 ? __ldg(p.scales + mine.adapter) : 0.0f;
+    }
+    tc_fence_before();
+    cluster_arrive_relaxed(); // (all of the cluster runs before any shared memory of another CTA is touched)
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int cl = plan.cluster;
+    const int rank = (int)cluster_ctarank();
+    const int total_segs =
+        __popc(warp_starts[0]) + __popc(warp_starts[1]) + __popc(warp_starts[2]) + __popc(warp_starts[3]);
+    // this CTA's shares: every cl-th block of k and of columns, so that the
+    // cluster as a whole reads and writes long runs of each row
+    const int kbs = ((p.K + WIDE_BK - 1) / WIDE_BK - rank + cl - 1) / cl;
+    const int n_tiles = ((p.N + 127) / 128 - rank + cl - 1) / cl;
+    const int chunks = (p.R + 63) / 64;
+    const int pitch = p.R + 4; // floats per row of the exchanged shares
+
+    // ring positions, kept over the passes by each role
+    uint32_t it2 = 0, pass_it = 0;
+    uint32_t acc_phase = 0; // bit b: parity of accumulator b
+    uint32_t phase1 = 0; // bit s: parity of stage s of the first ring (the ring restarts with each pass)
+    const uint32_t s2 = (uint32_t)plan.stages2;
+    bool ok = true;
+    cluster_wait();
+
+    for (int seg0 = 0; seg0 < total_segs; seg0 += plan.segs, ++pass_it) {
+        const int segs = min(plan.segs, total_segs - seg0);
+        const uint32_t stage_bytes = 2 * (WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes);
+        const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 1
+        // a walk along the first ring: stage, and which of its uses in this pass is odd
+        struct Ring {
+            int s, stages;
+            uint32_t odd;
+            __device__ __forceinline__ void skip(int n)
+            {
+                s += n;
+                while (s >= stages) {
+                    s -= stages;
+                    odd ^= 1u;
+                }
+            }
+        };
+        auto parity1 = [&](const Ring &r) { return ((phase1 >> r.s) ^ r.odd) & 1u; };
+        auto load_b = [&](int t, int i, int rc) { // stage it2 of the B ring
+            const uint32_t s = it2 % s2; // (of the B ring)
+            if (!ok || !(ok = wait(&empty2[s], ((it2 / s2) & 1) ^ 1)))
+                return;
+            mbar_arrive_expect_tx(&full2[s], WIDE_B_BYTES);
+            tma_load_nd<true, false>(smem + plan.off_b + s * WIDE_B_BYTES, &tmap_b, smem_addr(&full2[s]), rc * 64,
+                                     (t * cl + rank) * 128, seg_adapter[seg0 + i]);
+            ++it2;
+        };
+        // accumulators: two while a pass has at most two adapters (512 columns
+        // of tensor memory), else one
+        auto acc_buf = [&](int t) { return segs <= 2 ? t & 1 : 0; };
+        auto acc_parity = [&](int t) { return ((acc_phase >> acc_buf(t)) ^ (uint32_t)(segs <= 2 ? t >> 1 : t)) & 1u; };
+        const int b_loads = n_tiles * segs * chunks;
+        int b_done = 0;
+
+        // ------------------------------------------------------------ phase 1
+        if (warp < 4) {
+            // thread: 16-byte piece lane % 8 of both halves of rows 32 warp + 4 j + lane / 8
+            const int piece = lane & 7;
+            const uint16_t *src[8];
+            uint32_t live = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = warp * 32 + 4 * j + (lane >> 3);
+                const int seg = slot_seg[r];
+                const bool in = seg >= seg0 && seg < seg0 + segs;
+                src[j] = static_cast<const uint16_t *>(p.x) + (in ? slot_row[r] * p.ld_x : 0) + piece * 8;
+                live |= (in ? 1u : 0u) << j;
+            }
+            const uint32_t dst = (uint32_t)((warp * 32 + (lane >> 3)) * 128);
+            // a stage is published once its copies have landed, `lag` rounds
+            // after they were issued
+            const int lag = min(2, s1 - 1);
+            Ring at = {0, s1, 0u}, behind = {0, s1, 0u};
+            auto publish = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&full1[behind.s]);
+                behind.skip(1);
+            };
+            for (int i = 0; ok && i < kbs; ++i, at.skip(1)) {
+                ok = wait(&empty1[at.s], parity1(at) ^ 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                const uint32_t to = base + at.s * stage_bytes + dst;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = (i * cl + rank) * WIDE_BK + h * 64;
+                    const bool k_in = k + piece * 8 < p.K;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = 4 * j + (lane >> 3); // (its low 3 bits are the row's)
+                        const bool in = k_in && ((live >> j) & 1u);
+                        cp_async_16(to + h * WIDE_X_BYTES + j * 512 + ((piece ^ (r & 7)) << 4),
+                                    in ? src[j] + k : static_cast<const uint16_t *>(p.x), in);
+                    }
+                }
+                cp_async_commit();
+                if (i >= lag) {
+                    if (lag == 2)
+                        cp_async_wait<2>();
+                    else if (lag == 1)
+                        cp_async_wait<1>();
+                    else
+                        cp_async_wait<0>();
+                    publish();
+                }
+            }
+            cp_async_wait<0>();
+            for (int i = min(lag, kbs); ok && i > 0; --i)
+                publish();
+        } else if (warp == 5) {
+            if (lane == 0) {
+                Ring at = {0, s1, 0u};
+                for (int i = 0; ok && i < kbs; ++i, at.skip(1)) {
+                    const int s = at.s;
+                    if (!(ok = wait(&empty1[s], parity1(at) ^ 1u)))
+                        break;
+                    mbar_arrive_expect_tx(&full1[s], 2u * (uint32_t)segs * plan.a_bytes);
+                    for (int j = 0; j < 2 * segs; ++j) // (a half past K is zeros)
+                        tma_load_nd<true, false>(smem + s * stage_bytes + 2 * WIDE_X_BYTES + j * plan.a_bytes, &tmap_a,
+                                                 smem_addr(&full1[s]), (i * cl + rank) * WIDE_BK + (j & 1) * 64, 0,
+                                                 seg_adapter[seg0 + (j >> 1)]);
+                }
+                // the first stages of B, while the products of phase 1 run
+                for (; b_done < min(b_loads, (int)s2); ++b_done)
+                    load_b(b_done / (segs * chunks), b_done / chunks % segs, b_done % chunks);
+            }
+        } else if (warp == 4) {
+            if (lane == 0) {
+                Ring at = {0, s1, 0u};
+                for (int i = 0; ok && i < kbs; ++i, at.skip(1)) {
+                    const int s = at.s;
+                    if (!(ok = wait(&full1[s], parity1(at))))
+                        break;
+                    tc_fence_after();
+                    const uint32_t at_x = base + s * stage_bytes, at_a = at_x + 2 * WIDE_X_BYTES;
+                    for (int j = 0; j < segs; ++j) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t xd = make_sdesc(at_x + h * WIDE_X_BYTES);
+                            const uint64_t ad = make_sdesc(at_a + (2 * j + h) * plan.a_bytes);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16<false>(tmem + j * 128, xd + 2 * k, ad + 2 * k, wp.idesc1,
+                                               (i > 0 || h > 0 || k > 0) ? 1u : 0u);
+                        }
+                    }
+                    mma_commit(&empty1[s]);
+                }
+                mma_commit(p1_done);
+            }
+        } else if (warp >= 8) {
+            // this CTA's share of v: lane = slot
+            const int q = warp & 3, r = q * 32 + lane;
+            ok = wait(p1_done, pass_it & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc_fence_after();
+                const int mine = slot_seg[r] - seg0;
+                const uint32_t present = segments_present(mine, segs);
+                const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
+                const bool none = kbs == 0; // more CTAs than blocks of k
+                for (int c = (warp >= 12 ? 16 : 0); c < p.R; c += 32) { // two warps per 32 slots
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = 0.0f;
+                    for (uint32_t left = present; left; left &= left - 1) {
+                        const int i = __ffs(left) - 1;
+                        float w[16];
+                        tmem_ld16(taddr + i * 128 + c, w);
+                        tmem_wait_ld(w);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = mine == i ? w[j] : v[j];
+                    }
+                    const uint32_t to = base + (uint32_t)(r * pitch + c) * 4u;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        if (c + j < p.R)
+                            st_shared_v4(to + j * 4, none ? 0u : __float_as_uint(v[j]),
+                                         none ? 0u : __float_as_uint(v[j + 1]), none ? 0u : __float_as_uint(v[j + 2]),
+                                         none ? 0u : __float_as_uint(v[j + 3]));
+                }
+                tc_fence_before();
+            }
+        }
+        __syncwarp();
+
+        // ------------------------------------------------------------ exchange
+        // An epilogue warp has 32 slots and half of a tile's columns; its lanes
+        // move whole 128-byte lines of c and d, 8 lanes each: slots er + 4 i +
+        // lane / 8.  The first tile's c is on its way during the exchange where
+        // its buffers lie behind the shares.
+        const int er = (warp & 3) * 32, half = warp >= 12 ? 1 : 0;
+        int rows[8]; // -1: not in this pass
+        if (warp >= 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = er + 4 * i + (lane >> 3);
+                const int seg = slot_seg[r];
+                rows[i] = seg >= seg0 && seg < seg0 + segs ? slot_row[r] : -1;
+            }
+        }
+        const int piece = half * 8 + (lane & 7); // of a slot's 16 pieces of 16 bytes
+        // piece i of slot r in buffer b, spread over the banks
+        auto c_at = [&](int b, int r, int i) {
+            return base + plan.off_c + (uint32_t)(b * WIDE_C_BYTES + r * 256 + ((i ^ (r & 7)) << 4));
+        };
+        auto fetch_c = [&](int t) {
+            const int col = (t * cl + rank) * 128 + piece * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (rows[i] >= 0 && col < p.N)
+                    cp_async_16(c_at(t & 1, er + 4 * i + (lane >> 3), piece),
+                                static_cast<const uint16_t *>(p.c) + (long)rows[i] * p.ld_c + col, true);
+            cp_async_commit();
+        };
+        const bool early = plan.off_c > 0;
+        if (early && warp >= 8 && n_tiles > 0)
+            fetch_c(0);
+        cluster_sync(); // every CTA's share is there
+        // this CTA's part of the slots, two per round of a warp
+        const int part = WIDE_SLOTS / cl;
+        for (int i = warp; i < part; i += 2 * WIDE_WARPS) {
+            const int rk = lane * 4;
+            float4 v[2][8];
+            int seg[2], r[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                r[h] = rank * part + i + h * WIDE_WARPS;
+                seg[h] = i + h * WIDE_WARPS < part ? slot_seg[r[h]] : -1;
+                if (seg[h] < seg0 || seg[h] >= seg0 + segs)
+                    seg[h] = -1;
+                const uint32_t at = base + (uint32_t)(r[h] * pitch + rk) * 4u;
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    v[h][z] = z < cl && seg[h] >= 0 && rk < p.R ? ld_shared_cluster_v4(map_shared_rank(at, (uint32_t)z))
+                                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (seg[h] < 0)
+                    continue;
+                float4 sum = v[h][0];
+#pragma unroll
+                for (int z = 1; z < 8; ++z) {
+                    sum.x += v[h][z].x;
+                    sum.y += v[h][z].y;
+                    sum.z += v[h][z].z;
+                    sum.w += v[h][z].w;
+                }
+                float scale = 1.0f;
+                if constexpr (!BF16)
+                    scale = lora_fp16_scale(
+                        fmaxf(fmaxf(fabsf(sum.x), fabsf(sum.y)), fmaxf(fabsf(sum.z), fabsf(sum.w))));
+                const float inv = 1.0f / scale; // a power of two: exact
+                uint32_t hi[2], lo[2];
+                split_two<BF16>(sum.x * inv, sum.y * inv, hi[0], lo[0]);
+                split_two<BF16>(sum.z * inv, sum.w * inv, hi[1], lo[1]);
+                const uint32_t at = base + plan.off_v + (uint32_t)((rk >> 6) * WIDE_X_BYTES + r[h] * 128 +
+                                                                   ((((rk & 63) >> 3) ^ (r[h] & 7)) << 4) + (rk & 7) * 2);
+                const float f = scale * adapter_scale[r[h]];
+                for (int z = 0; z < cl; ++z) {
+                    if (rk < chunks * 64) {
+                        const uint32_t to = map_shared_rank(at, (uint32_t)z);
+                        st_cluster_v2(to, hi[0], hi[1]);
+                        st_cluster_v2(to + chunks * WIDE_X_BYTES, lo[0], lo[1]);
+                    }
+                    if (lane == 0)
+                        st_cluster_f32(map_shared_rank(smem_addr(&slot_scale[r[h]]), (uint32_t)z), f);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        cluster_sync(); // v is in every CTA, and nobody reads the shares any more
+        fence_proxy_async_smem();
+        if (!early && warp >= 8 && n_tiles > 0)
+            fetch_c(0);
+
+        // ------------------------------------------------------------ phase 2
+        if (warp == 5) {
+            if (lane == 0)
+                for (; ok && b_done < b_loads; ++b_done)
+                    load_b(b_done / (segs * chunks), b_done / chunks % segs, b_done % chunks);
+        } else if (warp == 4) {
+            if (lane == 0) {
+                tc_fence_after();
+                for (int t = 0; ok && t < n_tiles; ++t) {
+                    const int buf = acc_buf(t);
+                    if (!(ok = wait(&acc_empty[buf], acc_parity(t) ^ 1u)))
+                        break;
+                    for (int i = 0; ok && i < segs; ++i) {
+                        const uint32_t d = tmem + (buf * segs + i) * 128;
+                        for (int rc = 0; rc < chunks; ++rc, ++it2) {
+                            const uint32_t s = it2 % s2;
+                            if (!(ok = wait(&full2[s], (it2 / s2) & 1)))
+                                break;
+                            tc_fence_after();
+                            const uint64_t bd = make_sdesc(base + plan.off_b + s * WIDE_B_BYTES);
+                            const int steps = min(4, (p.R - rc * 64 + 15) / 16);
+#pragma unroll
+                            for (int term = 0; term < 2; ++term) {
+                                const uint64_t vd =
+                                    make_sdesc(base + plan.off_v + (uint32_t)(term * chunks + rc) * WIDE_X_BYTES);
+                                for (int k = 0; k < steps; ++k)
+                                    mma_f16<false>(d, vd + 2 * k, bd + 2 * k, wp.idesc2,
+                                                   (rc > 0 || term > 0 || k > 0) ? 1u : 0u);
+                            }
+                            mma_commit(&empty2[s]);
+                        }
+                    }
+                    mma_commit(&acc_full[buf]);
+                }
+            }
+        } else if (warp >= 8) {
+            const int q = warp & 3, r = q * 32 + lane;
+            const int mine = slot_seg[r] - seg0;
+            const uint32_t present = segments_present(mine, segs);
+            const float f = (mine >= 0 && mine < segs) ? slot_scale[r] : 0.0f;
+            for (int t = 0; t < n_tiles; ++t) {
+                if (t + 1 < n_tiles) {
+                    fetch_c(t + 1);
+                    cp_async_wait<1>();
+                } else {
+                    cp_async_wait<0>();
+                }
+                __syncwarp(); // every lane's pieces of c are there
+                const int buf = acc_buf(t);
+                ok = wait(&acc_full[buf], acc_parity(t));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + buf * segs * 128 + half * 64;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float v[32];
+                    for (uint32_t left = present; left; left &= left - 1) {
+                        const int i = __ffs(left) - 1;
+                        if (left == present) { // the first, usually the only one
+                            tmem_ld32(taddr + i * 128 + c, v);
+                            tmem_wait_ld(v);
+                        } else {
+                            float w[32];
+                            tmem_ld32(taddr + i * 128 + c, w);
+                            tmem_wait_ld(w);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = mine == i ? w[j] : v[j];
+                        }
+                    }
+                    if (c == 32) { // the accumulator has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&acc_empty[buf]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        const uint32_t at = c_at(t & 1, r, half * 8 + ((c + j) >> 3));
+                        const uint4 in = ld_shared_v4(at);
+                        const uint32_t old[4] = {in.x, in.y, in.z, in.w};
+                        uint32_t out[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 o = unpack2<BF16>(old[i]);
+                            out[i] = pack2<BF16>(fmaf(f, v[j + 2 * i], o.x), fmaf(f, v[j + 2 * i + 1], o.y));
+                        }
+                        st_shared_v4(at, out[0], out[1], out[2], out[3]);
+                    }
+                }
+                __syncwarp();
+                const int col = (t * cl + rank) * 128 + piece * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (rows[i] >= 0 && col < p.N) {
+                        const uint4 o = ld_shared_v4(c_at(t & 1, er + 4 * i + (lane >> 3), piece));
+                        st_global_v4(static_cast<uint16_t *>(p.d) + (long)rows[i] * p.ld_d + col, o.x, o.y, o.z, o.w);
+                    }
+                __syncwarp();
+            }
+            cp_async_wait<0>();
+        }
+        __syncwarp();
+        for (int s = 0; s < s1 && s < kbs; ++s)
+            phase1 ^= (uint32_t)((kbs - s + s1 - 1) / s1 & 1) << s;
+        if (segs <= 2)
+            acc_phase ^= (uint32_t)((n_tiles + 1) >> 1 & 1) | (uint32_t)(n_tiles >> 1 & 1) << 1;
+        else
+            acc_phase ^= (uint32_t)(n_tiles & 1);
+        // ordinary accesses of the rings come before the next pass's TMA writes
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
+
+    // all MMAs complete before tensor memory is released; where a wait ran out,
+    // copies that nothing waited for land before the CTA exits
+    if (warp == 4 && lane == 0) {
+        mma_commit(mma_done);
+        const uint32_t a = smem_addr(mma_done);
+        if (!mbar_try_wait(a, 0))
+            wait_slow(a, 0, abort_flag, p.status, wp.timeout_ns, false);
+        if (*abort_flag) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {
+            }
+        }
+    }
+    cluster_sync(); // nobody leaves while another CTA may still use its shared memory
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Shared memory of a call: see the kernel's phases.
+WidePlan wide_plan(int slots, int R)
+{
+    WidePlan w = {};
+    const int blocks = (slots + WIDE_SLOTS - 1) / WIDE_SLOTS;
+    // as many CTAs per block of slots as run at once (clusters of 8, 4 and 2
+    // with one CTA per SM that a 148-SM part holds: 15, 33 and 74)
+    w.cluster = blocks <= 15 ? 8 : blocks <= 33 ? 4 : blocks <= 74 ? 2 : 1;
+    const uint32_t chunks = (uint32_t)(R + 63) / 64;
+    w.segs = R <= 64 ? 4 : 1;
+    w.a_bytes = (uint32_t)(R + 15) / 16 * 16 * 128;
+    // three stages with one adapter, two with two and one with four up to rank
+    // 64, one or two above; the shares (at most 68 KB) and two c buffers (64
+    // KB, beside the shares up to rank 64) in the same room
+    w.ring = R <= 64 ? 3u * 49152u : 98304u;
+    w.off_c = R <= 64 ? align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024) : 0;
+    w.off_v = w.ring;
+    w.off_b = w.off_v + 2 * chunks * WIDE_X_BYTES;
+    w.stages2 = R <= 64 ? 2 : 3;
+    w.off_bars = w.off_b + (uint32_t)w.stages2 * WIDE_B_BYTES;
+    w.total = w.off_bars + 8u * (4u * WIDE_MAX_STAGES + 6u);
+    return w;
+}
+
+template <bool BF16>
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParams &wp, const DeviceView &dev,
+                   cudaStream_t stream)
+{
+    static std::atomic<bool> ready[64];
+    auto kernel = lora_wide_kernel<BF16>;
+    const int smem = (int)wp.plan.total + 1024;
+    if (!ready[dev.index].load(std::memory_order_acquire)) {
+        const cudaError_t err =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem - 4096);
+        if (err != cudaSuccess)
+            return err;
+        ready[dev.index].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)wp.plan.cluster, (unsigned)((wp.p.slots + WIDE_SLOTS - 1) / WIDE_SLOTS), 1);
+    cfg.blockDim = dim3(WIDE_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)wp.plan.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, ta, tb, wp);
+}
+
+} // namespace
+
+// Long batches with enough slots per adapter; grid.y counts blocks of slots.
+bool lora_is_wide(int slots, int adapters, int R)
+{
+    return slots > 256 && R <= 128 && slots / adapters >= 32 && slots <= 65535 * WIDE_SLOTS;
+}
+
+int launch_lora_wide(const LoraParams &p, bool bf16, const DeviceView &dev, cudaStream_t stream)
+{
+    WideParams wp;
+    memset(&wp, 0, sizeof(wp));
+    wp.p = p;
+    wp.plan = wide_plan(p.slots, p.R);
+    if ((int)wp.plan.total + 1024 > dev.max_smem - 4096)
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    const int ranks = (p.R + 15) / 16 * 16;
+    wp.idesc1 = ragged_idesc(bf16, false, false, 128, ranks);
+    wp.idesc2 = ragged_idesc(bf16, false, false, 128, 128);
+    wp.timeout_ns = dev.timeout_ns;
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap ta, tb;
+    {
+        const uint64_t dims[3] = {(uint64_t)p.K, (uint64_t)p.R, (uint64_t)p.adapters};
+        const uint64_t strides[2] = {(uint64_t)p.K * 2, (uint64_t)p.R * (uint64_t)p.K * 2};
+        const uint32_t box[3] = {64, (uint32_t)ranks, 1};
+        const int st = make_tmap_128b(&ta, p.lora_a, type, 3, dims, strides, box);
+        if (st != DG_OK)
+            return st;
+    }
+    {
+        const uint64_t dims[3] = {(uint64_t)p.R, (uint64_t)p.N, (uint64_t)p.adapters};
+        const uint64_t strides[2] = {(uint64_t)p.R * 2, (uint64_t)p.N * (uint64_t)p.R * 2};
+        const uint32_t box[3] = {64, 128, 1};
+        const int st = make_tmap_128b(&tb, p.lora_b, type, 3, dims, strides, box);
+        if (st != DG_OK)
+            return st;
+    }
+    const cudaError_t err = bf16 ? launch<true>(ta, tb, wp, dev, stream) : launch<false>(ta, tb, wp, dev, stream);
+    return err == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+} // namespace fp8nt

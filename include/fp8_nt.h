@@ -230,9 +230,9 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups);
  * A value out of range sets DG_ERR_DEVICE_BAD_INDEX and its slot is skipped.
  * rank: a multiple of 8, at most 256 (smaller adapters: zero rows of A and
  * columns of B); N % 8 == 0, K % 8 == 0.  workspace: at least
- * get_lora_workspace_size(num_slots, rank, N, K) bytes, 16-byte aligned, in use
- * until the call's work has completed; calls that may run at the same time
- * need one each. */
+ * get_lora_workspace_size(num_slots, num_adapters, rank, N, K) bytes (0 for
+ * long batches), 16-byte aligned, in use until the call's work has completed;
+ * calls that may run at the same time need one each. */
 int m_grouped_lora_add(const void *X, long long ld_x, const void *A, const void *B,
                        const float *scales, const void *C, long long ld_c, void *D, long long ld_d,
                        const int *m_indices, const int *order, int dtype, int num_slots,
@@ -241,7 +241,7 @@ int m_grouped_lora_add(const void *X, long long ld_x, const void *A, const void 
 
 /* Bytes of workspace m_grouped_lora_add needs; negative dg_status on a bad
  * argument. */
-long long get_lora_workspace_size(int num_slots, int rank, int N, int K);
+long long get_lora_workspace_size(int num_slots, int num_adapters, int rank, int N, int K);
 
 /* Row alignment of each expert segment in the contiguous layout (DeepGEMM
  * README, utility functions: get_m_alignment_for_contiguous_layout).  128. */

@@ -78,9 +78,11 @@ def test_group_sizes_and_refusals(lib):
 
 
 def test_lora_sizes_and_refusals(lib):
-    assert fp8.get_lora_workspace_size(0, 16, 64, 64) == 0
-    assert fp8.get_lora_workspace_size(64, 16, 64, 7168) >= 64 * 16 * 4
-    for args in ((4, 12, 64, 64), (4, 264, 64, 64), (4, 0, 64, 64), (4, 16, 60, 64), (4, 16, 64, 4), (-1, 16, 64, 64)):
+    assert fp8.get_lora_workspace_size(0, 2, 16, 64, 64) == 0
+    assert fp8.get_lora_workspace_size(64, 2, 16, 64, 7168) >= 64 * 16 * 4
+    assert fp8.get_lora_workspace_size(4096, 8, 16, 64, 7168) == 0   # long batches need none
+    for args in ((4, 2, 12, 64, 64), (4, 2, 264, 64, 64), (4, 2, 0, 64, 64), (4, 2, 16, 60, 64), (4, 2, 16, 64, 4),
+                 (-1, 2, 16, 64, 64), (4, 0, 16, 64, 64)):
         with pytest.raises(fp8.Fp8NtError):
             fp8.get_lora_workspace_size(*args)
 
