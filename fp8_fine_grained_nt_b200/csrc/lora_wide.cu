@@ -12,7 +12,7 @@
 //
 //   phase 1   four warps gather the slots' rows of x into a ring (cp.async,
 //             written in the layout the MMA reads), TMA brings A; M = 128
-//             slots, N = rank, 128 of k per stage.
+//             slots, N = rank.
 //   exchange  each CTA puts its FP32 share of v into its shared memory; after
 //             a cluster barrier every CTA adds the shares of its part of the
 //             slots in rank order, splits v into two 16-bit terms and writes
@@ -48,7 +48,6 @@ constexpr int WIDE_SLOTS = 128;
 constexpr int WIDE_THREADS = 512;
 constexpr int WIDE_WARPS = WIDE_THREADS / 32;
 constexpr int WIDE_MAX_STAGES = 8;
-constexpr int WIDE_BK = 128;                        // k per stage: two 64-wide swizzled halves
 constexpr uint32_t WIDE_X_BYTES = WIDE_SLOTS * 128; // 128 rows of 64 elements
 constexpr uint32_t WIDE_B_BYTES = 128 * 128;        // 128 columns x 64 ranks
 constexpr uint32_t WIDE_C_BYTES = WIDE_SLOTS * 256; // 128 slots x 128 columns
@@ -193,8 +192,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const int total_segs =
         __popc(warp_starts[0]) + __popc(warp_starts[1]) + __popc(warp_starts[2]) + __popc(warp_starts[3]);
     // this CTA's shares: every cl-th block of k and of columns, so that the
-    // cluster as a whole reads and writes long runs of each row
-    const int kbs = ((p.K + WIDE_BK - 1) / WIDE_BK - rank + cl - 1) / cl;
+    // cluster as a whole reads and writes long runs of each row (kbs below)
     const int n_tiles = ((p.N + 127) / 128 - rank + cl - 1) / cl;
     const int chunks = (p.R + 63) / 64;
     const int pitch = p.R + 4; // floats per row of the exchanged shares
@@ -209,8 +207,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
     for (int seg0 = 0; seg0 < total_segs; seg0 += plan.segs, ++pass_it) {
         const int segs = min(plan.segs, total_segs - seg0);
-        const uint32_t stage_bytes = 2 * (WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes);
-        const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 1
+        // 128 of k per stage (two 64-wide swizzled halves: fewer waits) where
+        // three such stages fit, else 64
+        const uint32_t half_bytes = WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes;
+        const int halves = 6 * half_bytes <= plan.ring ? 2 : 1, bk = 64 * halves;
+        const uint32_t stage_bytes = halves * half_bytes;
+        const int kbs = ((p.K + bk - 1) / bk - rank + cl - 1) / cl;
+        const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 3
         // a walk along the first ring: stage, and which of its uses in this pass is odd
         struct Ring {
             int s, stages;
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const uint32_t dst = (uint32_t)((warp * 32 + (lane >> 3)) * 128);
             // a stage is published once its copies have landed, `lag` rounds
             // after they were issued
-            const int lag = min(2, s1 - 1);
+            constexpr int lag = 2; // less than the stages there are
             Ring at = {0, s1, 0u}, behind = {0, s1, 0u};
             auto publish = [&]() {
                 fence_proxy_async_smem();
@@ -273,9 +276,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (!ok)
                     break;
                 const uint32_t to = base + at.s * stage_bytes + dst;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = (i * cl + rank) * WIDE_BK + h * 64;
+                for (int h = 0; h < halves; ++h) {
+                    const int k = (i * cl + rank) * bk + h * 64;
                     const bool k_in = k + piece * 8 < p.K;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -287,12 +289,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 cp_async_commit();
                 if (i >= lag) {
-                    if (lag == 2)
-                        cp_async_wait<2>();
-                    else if (lag == 1)
-                        cp_async_wait<1>();
-                    else
-                        cp_async_wait<0>();
+                    cp_async_wait<lag>();
                     publish();
                 }
             }
@@ -306,11 +303,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     const int s = at.s;
                     if (!(ok = wait(&empty1[s], parity1(at) ^ 1u)))
                         break;
-                    mbar_arrive_expect_tx(&full1[s], 2u * (uint32_t)segs * plan.a_bytes);
-                    for (int j = 0; j < 2 * segs; ++j) // (a half past K is zeros)
-                        tma_load_nd<true, false>(smem + s * stage_bytes + 2 * WIDE_X_BYTES + j * plan.a_bytes, &tmap_a,
-                                                 smem_addr(&full1[s]), (i * cl + rank) * WIDE_BK + (j & 1) * 64, 0,
-                                                 seg_adapter[seg0 + (j >> 1)]);
+                    mbar_arrive_expect_tx(&full1[s], (uint32_t)(halves * segs) * plan.a_bytes);
+                    uint8_t *dst = smem + s * stage_bytes + halves * WIDE_X_BYTES;
+                    for (int h = 0; h < halves; ++h) // (a half past K is zeros)
+                        for (int j = 0; j < segs; ++j, dst += plan.a_bytes)
+                            tma_load_nd<true, false>(dst, &tmap_a, smem_addr(&full1[s]),
+                                                     (i * cl + rank) * bk + h * 64, 0, seg_adapter[seg0 + j]);
                 }
                 // the first stages of B, while the products of phase 1 run
                 for (; b_done < min(b_loads, (int)s2); ++b_done)
@@ -324,12 +322,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     if (!(ok = wait(&full1[s], parity1(at))))
                         break;
                     tc_fence_after();
-                    const uint32_t at_x = base + s * stage_bytes, at_a = at_x + 2 * WIDE_X_BYTES;
-                    for (int j = 0; j < segs; ++j) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint64_t xd = make_sdesc(at_x + h * WIDE_X_BYTES);
-                            const uint64_t ad = make_sdesc(at_a + (2 * j + h) * plan.a_bytes);
+                    const uint32_t at_x = base + s * stage_bytes;
+                    uint32_t at_a = at_x + halves * WIDE_X_BYTES;
+                    for (int h = 0; h < halves; ++h) {
+                        const uint64_t xd = make_sdesc(at_x + h * WIDE_X_BYTES);
+                        for (int j = 0; j < segs; ++j, at_a += plan.a_bytes) {
+                            const uint64_t ad = make_sdesc(at_a);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_f16<false>(tmem + j * 128, xd + 2 * k, ad + 2 * k, wp.idesc1,
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 const int mine = slot_seg[r] - seg0;
                 const uint32_t present = segments_present(mine, segs);
                 const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16);
-                const bool none = kbs == 0; // more CTAs than blocks of k
+                const bool none = kbs <= 0; // more CTAs than blocks of k
                 for (int c = (warp >= 12 ? 16 : 0); c < p.R; c += 32) { // two warps per 32 slots
                     float v[16];
 #pragma unroll
@@ -616,8 +614,8 @@ WidePlan wide_plan(int slots, int R)
     const uint32_t chunks = (uint32_t)(R + 63) / 64;
     w.segs = R <= 64 ? 4 : 1;
     w.a_bytes = (uint32_t)(R + 15) / 16 * 16 * 128;
-    // three stages with one adapter, two with two and one with four up to rank
-    // 64, one or two above; the shares (at most 68 KB) and two c buffers (64
+    // at least three stages of 64 of k (four adapters, or one above rank 64),
+    // three of 128 with one adapter up to rank 64; the shares (at most 68 KB) and two c buffers (64
     // KB, beside the shares up to rank 64) in the same room
     w.ring = R <= 64 ? 3u * 49152u : 98304u;
     w.off_c = R <= 64 ? align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024) : 0;
