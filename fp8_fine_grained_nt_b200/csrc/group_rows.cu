@@ -5,8 +5,8 @@
 //   slot(r) = offsets[g] + number of rows r' < r with the same group g
 //
 // Bound by latency for a decode step (a few hundred rows) and by the ranks of
-// the rows for a long prefill (the arrays are a few MB).  Up to GROUP_CHUNK
-// rows, one CTA does everything in one launch.  Beyond that the rows are cut
+// the rows for a long prefill (the arrays are a few MB).  A short call is
+// done by one CTA in one launch.  Beyond that the rows are cut
 // into contiguous chunks: one kernel counts each chunk's rows per group, a
 // second one adds up the counts of the chunks before its own and places its
 // rows.  No atomics on global memory: the result does not depend on timing.
@@ -27,6 +27,7 @@ namespace {
 
 constexpr int GROUP_THREADS = 512;
 constexpr int GROUP_WARPS = GROUP_THREADS / 32;
+constexpr int GROUP_BATCH = 8; // rows per lane whose groups are read at once
 
 struct GroupArgs {
     const void *index;
@@ -74,10 +75,17 @@ __device__ __forceinline__ void count_chunk(const GroupArgs &a, int r0, int r1, 
     const int per = a.chunk / GROUP_WARPS;
     const int w0 = r0 + warp * per, w1 = min(w0 + per, r1);
     int *mine = hist + warp * a.groups;
-    for (int r = w0 + lane; r < w1; r += 32) {
-        const int g = group_of<I64>(a, r, bad);
-        if (g >= 0)
-            atomicAdd(mine + g, 1);
+    for (int base = w0; base < w1; base += 32 * GROUP_BATCH) {
+        int g[GROUP_BATCH];
+#pragma unroll
+        for (int i = 0; i < GROUP_BATCH; ++i) {
+            const int r = base + 32 * i + lane;
+            g[i] = r < w1 ? group_of<I64>(a, r, bad) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP_BATCH; ++i)
+            if (g[i] >= 0)
+                atomicAdd(mine + g[i], 1);
     }
     __syncthreads();
 }
@@ -124,23 +132,35 @@ __global__ void __launch_bounds__(GROUP_THREADS) group_place_kernel(const GroupA
         grid_dependency_wait();
         grid_launch_dependents();
     }
-    // rows of each group in all chunks and in those before this one (kept in
+    // rows of each group in all chunks, and in those before this one (in
     // start[] until the scan)
-    for (int g = tid; g < G; g += GROUP_THREADS) {
-        int all = 0, before = 0;
-        if (a.chunks == 1) {
+    if (a.chunks == 1) {
+        for (int g = tid; g < G; g += GROUP_THREADS) {
+            int all = 0;
+#pragma unroll
             for (int w = 0; w < GROUP_WARPS; ++w)
                 all += hist[w * G + g];
-        } else {
+            total[g] = all;
+            start[g] = 0;
+        }
+    } else {
+        // all threads share the sums of a group: `parts` runs of chunks each
+        const int parts = max(1, GROUP_THREADS / G), per = (a.chunks + parts - 1) / parts;
+        for (int g = tid; g < G; g += GROUP_THREADS)
+            total[g] = start[g] = 0;
+        __syncthreads();
+        for (int i = tid; i < G * parts; i += GROUP_THREADS) {
+            const int g = i % G, c0 = i / G * per, c1 = min(c0 + per, a.chunks);
+            int all = 0, before = 0;
 #pragma unroll 8
-            for (int c = 0; c < a.chunks; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 const int n = __ldcg(a.counts + (size_t)c * G + g);
                 all += n;
                 before += c < (int)blockIdx.x ? n : 0;
             }
+            atomicAdd(total + g, all); // whole numbers: any order gives the same
+            atomicAdd(start + g, before);
         }
-        total[g] = all;
-        start[g] = before;
     }
     __syncthreads();
     // exclusive scan of the padded totals; thread t owns `per` groups
@@ -160,15 +180,20 @@ __global__ void __launch_bounds__(GROUP_THREADS) group_place_kernel(const GroupA
         part[warp] = incl;
     __syncthreads();
     int at = incl - mine;
-    for (int w = 0; w < warp; ++w)
-        at += part[w];
+#pragma unroll
+    for (int w = 0; w < GROUP_WARPS; ++w)
+        at += w < warp ? part[w] : 0;
     for (int g = g0; g < g1; ++g) {
         // the next free slot of every warp's rows of group g
+        int n[GROUP_WARPS];
+#pragma unroll
+        for (int w = 0; w < GROUP_WARPS; ++w)
+            n[w] = hist[w * G + g];
         int next = at + start[g];
+#pragma unroll
         for (int w = 0; w < GROUP_WARPS; ++w) {
-            const int n = hist[w * G + g];
             hist[w * G + g] = next;
-            next += n;
+            next += n[w];
         }
         start[g] = at;
         if (blockIdx.x == 0)
@@ -187,23 +212,33 @@ __global__ void __launch_bounds__(GROUP_THREADS) group_place_kernel(const GroupA
         const int w0 = r0 + warp * per_warp, w1 = min(w0 + per_warp, r1);
         int *next = hist + warp * G;
         bool ignore = false;
-        for (int base = w0; base < w1; base += 32) {
-            const int r = base + lane;
-            const int g = r < w1 ? group_of<I64>(a, r, ignore) : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, g);
-            int slot = -1;
-            if (g >= 0) {
-                slot = next[g] + __popc(same & ((1u << lane) - 1u));
-                a.order[slot] = r;
-                if (a.m_indices)
-                    a.m_indices[slot] = g;
+        for (int base = w0; base < w1; base += 32 * GROUP_BATCH) {
+            int g[GROUP_BATCH];
+#pragma unroll
+            for (int i = 0; i < GROUP_BATCH; ++i) {
+                const int r = base + 32 * i + lane;
+                g[i] = r < w1 ? group_of<I64>(a, r, ignore) : -1;
             }
-            if (a.slots && r < w1)
-                a.slots[r] = slot;
-            __syncwarp();
-            if (g >= 0 && lane == 31 - __clz(same)) // the last of its group
-                next[g] = slot + 1;
-            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < GROUP_BATCH; ++i) {
+                if (base + 32 * i >= w1)
+                    break;
+                const int r = base + 32 * i + lane;
+                const uint32_t same = __match_any_sync(0xffffffffu, g[i]);
+                int slot = -1;
+                if (g[i] >= 0) {
+                    slot = next[g[i]] + __popc(same & ((1u << lane) - 1u));
+                    a.order[slot] = r;
+                    if (a.m_indices)
+                        a.m_indices[slot] = g[i];
+                }
+                if (a.slots && r < w1)
+                    a.slots[r] = slot;
+                __syncwarp();
+                if (g[i] >= 0 && lane == 31 - __clz(same)) // the last of its group
+                    next[g[i]] = slot + 1;
+                __syncwarp();
+            }
         }
     }
     // slots that hold no row: the padding of each group (groups dealt out to
@@ -260,14 +295,17 @@ cudaError_t launch(const GroupArgs &a, int device, cudaStream_t stream)
 
 } // namespace
 
-// Rows per chunk: 4096 (one CTA), growing so that at most 256 chunks' counts
-// are added up by every CTA.
+// Rows per chunk, a multiple of GROUP_THREADS: up to 2048 rows in one chunk
+// (one launch), else chunks of 2048, growing so that at most 256 chunks'
+// counts are added up by every CTA.
 int group_rows_chunk(int rows)
 {
-    const int most = 256;
-    const int chunk = (rows + most - 1) / most;
-    const int unit = GROUP_THREADS * 8;
-    return chunk <= unit ? unit : (chunk + unit - 1) / unit * unit;
+    const int most = 256, unit = 4 * GROUP_THREADS;
+    int chunk = rows <= unit ? rows : (rows + most - 1) / most;
+    if (rows > unit && chunk < unit)
+        chunk = unit;
+    chunk = (chunk + GROUP_THREADS - 1) / GROUP_THREADS * GROUP_THREADS;
+    return chunk > 0 ? chunk : GROUP_THREADS;
 }
 
 cudaError_t launch_group_rows(const void *index, bool i64, int rows, int groups, int alignment, int capacity,
