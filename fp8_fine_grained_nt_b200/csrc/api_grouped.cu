@@ -144,7 +144,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
 
     // shared memory: the deepest operand ring beside the output staging
     const uint32_t stage = 128u * 128u + y_rows * 128u;
-    const int slots = k->swap ? 0 : k->pair && !tn ? 1 : 2;
+    const int slots = k->swap ? 0 : k->pair ? 1 : 2;
     int stages = RAGGED_MAX_STAGES;
     for (; stages >= 2; --stages) {
         make_ragged_plan(p, stage, stages, slots);

@@ -23,9 +23,10 @@
 //          token rows are Y: for few rows per group, where the call is bound
 //          by reading the weights and 128 token rows would be mostly padding.
 //
-// Roles (256 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
-// only), warps 4-7 epilogue (one 32-lane quarter of tensor memory each).  Two
+// only), warps 4-11 epilogue (a 32-lane quarter of tensor memory and half of the
+// tile's columns each).  Two
 // accumulators in tensor memory let a tile's epilogue overlap the next
 // tile's MMAs.
 #pragma once
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], PAIR ? 8 : 4);
+            mbar_init(&acc_empty[b], PAIR ? 16 : 8);
         }
         mbar_init(mma_done, 1);
         misc[1] = 0u;
@@ -435,8 +436,11 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        const uint32_t taddr0 = tmem_base + ((uint32_t)(q * 32) << 16);
-        const uint32_t stg_w = smem_addr(smem + p.off_out) + (uint32_t)q * (uint32_t)p.out_slots * RAGGED_SLOT_BYTES;
+        constexpr int NC = BN / 2; // columns of this warp, from c_first on
+        const int c_first = warp >= 8 ? NC : 0;
+        const uint32_t taddr0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c_first;
+        const uint32_t stg_w =
+            smem_addr(smem + p.off_out) + (uint32_t)(warp - 4) * (uint32_t)p.out_slots * RAGGED_SLOT_BYTES;
         const bool bf16 = p.out_type == RAGGED_OUT_BF16;
         uint32_t tile_it = 0, slot = 0;
         for (int t = t_first; t < num_tiles; t += t_stride) {
@@ -457,18 +461,23 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 // a lane owns output column i0 + lane and the tile's token
                 // rows: 32 lanes store 64 consecutive bytes of a row
                 const int col = i0 + lane;
-                const int tok = min(BN, ti.rows - ti.j0);
-                uint16_t *dst = static_cast<uint16_t *>(p.d) + (size_t)(ti.first + ti.j0) * p.d_cols + col;
+                const int tok = min(NC, ti.rows - ti.j0 - c_first);
+                uint16_t *dst =
+                    static_cast<uint16_t *>(p.d) + (size_t)(ti.first + ti.j0 + c_first) * p.d_cols + col;
+                constexpr int W = NC < 32 ? NC : 32;
 #pragma unroll
-                for (int c = 0; c < BN; c += 32) {
+                for (int c = 0; c < NC; c += W) {
                     if (c >= tok)
                         break;
-                    float v[32];
-                    tmem_ld32(taddr + c, v);
+                    float v[W];
+                    if constexpr (W == 16)
+                        tmem_ld16(taddr + c, v);
+                    else
+                        tmem_ld32(taddr + c, v);
                     tmem_wait_ld(v);
                     if (col < p.d_cols) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < W; ++j)
                             if (c + j < tok)
                                 dst[(size_t)(c + j) * p.d_cols] = (uint16_t)pack_16x2(v[j], 0.0f, bf16);
                     }
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             const int row = TN ? i0 : ti.first + i0;
             const int width = f32 ? 32 : 64; // columns per 128-byte staged row
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 64) {
+            for (int c = 0; c < NC; c += 64) {
                 float v[2][32];
                 if (zero) {
 #pragma unroll
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     tmem_ld32(taddr + c + 32, v[1]);
                     tmem_wait_ld(v[0]);
                     reg_tie32(v[1]);
-                    if (c + 64 == BN) { // the accumulator has been read
+                    if (c + 64 == NC) { // the warp has read its part of the accumulator
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
@@ -526,7 +535,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 for (int h = 0; h < 2; ++h) {
                     if (!f32 && h == 1)
                         break;
-                    const int col = ti.j0 + c + h * 32;
+                    const int col = ti.j0 + c_first + c + h * 32;
                     // the slot's last store has read it
                     if (lane == 0) {
                         if (p.out_slots == 2)

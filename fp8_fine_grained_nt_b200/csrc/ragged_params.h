@@ -12,7 +12,7 @@ enum RaggedDir : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2 };
 enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 = 2 };
 
 constexpr int RAGGED_BK = 64;           // reduction elements per stage: 128-byte swizzled rows
-constexpr int RAGGED_THREADS = 256;     // 8 warps
+constexpr int RAGGED_THREADS = 384;     // 12 warps, 8 of them in the epilogue
 constexpr int RAGGED_MAX_STAGES = 12;
 constexpr int RAGGED_MAX_GROUPS = 1024;
 constexpr uint32_t RAGGED_SLOT_BYTES = 4096; // output staging: 32 rows of 128 bytes
@@ -48,10 +48,10 @@ inline void make_ragged_plan(RaggedParams &p, uint32_t stage_bytes, int stages, 
     p.stages = stages;
     p.out_slots = out_slots;
     p.off_out = stage_bytes * (uint32_t)stages;
-    p.off_groups = p.off_out + 4u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
+    p.off_groups = p.off_out + 8u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
     p.off_bars = align_up_u32(p.off_groups + 4u * (3u * (uint32_t)p.num_groups + 1u), 8);
     p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 5u), 16);
-    p.total = p.off_misc + 64;
+    p.total = p.off_misc + 80;
 }
 
 // tcgen05.mma kind::f16: FP32 result, both operands BF16 (or FP16), `mn` set
