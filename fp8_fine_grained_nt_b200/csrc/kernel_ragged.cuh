@@ -49,7 +49,7 @@ struct RaggedTraits {
     static constexpr uint32_t X_BYTES = 128 * 128;
     static constexpr uint32_t Y_BYTES = Y_ROWS * 128;
     static constexpr uint32_t STAGE_BYTES = X_BYTES + Y_BYTES;
-    static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int TMEM_COLS = 2 * BN;
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "power of two, at most 512");
 };
 
@@ -62,47 +62,65 @@ struct RaggedTile {
     int nkb;   // 64-wide blocks of the reduction
 };
 
-// Tile t.  `tiles` holds the tile prefix sums of the groups (NT, NN); order
-// within a group: bands of 8 X blocks, X fastest within a band, so that the
-// tiles in flight share both operands in L2.  SWAP: the token blocks of one
-// weight block run side by side.
+__device__ __forceinline__ int fast_div(int n, const FastDiv &f)
+{
+    return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
+}
+
+// Tile t.  `tiles` holds the tile prefix sums of the groups (NT, NN); `g` is
+// the group of the caller's previous (lower) tile.  Order within a group: bands
+// of 8 X blocks, X fastest within a band, so that the tiles in flight share
+// both operands in L2 (measured at 8192 x 8192 x 8192: bands of 8 741 us, of 4
+// 756 us, of 16 754 us).  SWAP: the token blocks of one weight block run side
+// by side.
 template <int DIR, bool SWAP, int BM, int BN>
-__device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, const int *tiles, const int *first,
-                                                  const int *count)
+__device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, int &g, const int *tiles,
+                                                  const int *first, const int *count)
 {
     RaggedTile r;
     int local, xb, yb;
     if (DIR == RAGGED_TN) {
-        r.g = t / p.tiles_per_group;
-        local = t - r.g * p.tiles_per_group;
+        g = fast_div(t, p.tiles_per_group);
+        local = t - g * (int)p.tiles_per_group.d;
         xb = p.x_blocks;
         yb = p.y_blocks;
     } else {
-        int lo = 0, hi = p.num_groups - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tiles[mid] <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
+        if (t >= tiles[g + 1]) {
+            int lo = g + 1, hi = p.num_groups - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (tiles[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            g = lo;
         }
-        r.g = lo;
-        local = t - tiles[lo];
-        const int tok_blocks = (count[lo] + (SWAP ? BN : BM) - 1) / (SWAP ? BN : BM);
+        local = t - tiles[g];
+        const int tok_blocks = (count[g] + (SWAP ? BN : BM) - 1) / (SWAP ? BN : BM);
         xb = SWAP ? p.x_blocks : tok_blocks;
         yb = SWAP ? tok_blocks : p.y_blocks;
     }
-    r.first = first[r.g];
-    r.rows = count[r.g];
+    r.g = g;
+    r.first = first[g];
+    r.rows = count[g];
     if (SWAP) {
-        r.i0 = local / yb * BM;
-        r.j0 = local % yb * BN;
+        const int q = yb == 1 ? local : local / yb;
+        r.i0 = q * BM;
+        r.j0 = (local - q * yb) * BN;
     } else {
-        const int band = local / (8 * yb);
-        const int in_band = local - band * 8 * yb;
-        const int width = min(8, xb - band * 8);
-        r.i0 = (band * 8 + in_band % width) * BM;
-        r.j0 = in_band / width * BN;
+        const int band = fast_div(local, p.band);
+        const int in_band = local - band * (int)p.band.d;
+        const int width = xb - band * 8;
+        int y;
+        if (width >= 8)
+            y = in_band >> 3;
+        else if (DIR == RAGGED_TN)
+            y = fast_div(in_band, p.last_band);
+        else
+            y = in_band / width;
+        r.i0 = (band * 8 + in_band - y * min(width, 8)) * BM;
+        r.j0 = y * BN;
     }
     r.nkb = DIR == RAGGED_TN ? (r.rows + RAGGED_BK - 1) / RAGGED_BK : p.nkb;
     return r;
@@ -267,20 +285,23 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = misc[0];
-    const int num_tiles = TN ? p.num_groups * p.tiles_per_group : tiles[p.num_groups];
+    const int num_tiles = TN ? p.num_groups * (int)p.tiles_per_group.d : tiles[p.num_groups];
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int t_first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
     const int t_stride = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
+    int group = 0; // of the role's current tile
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             uint32_t it = 0, s = 0, phase = 1;
-            uint32_t plain = 0; // per stage: its last use was counted on full[]
+            // per stage: its last use was counted on full[], and the parity of
+            // its uses of full[]
+            uint32_t plain = 0, uses = 0;
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
                 const int x_mn = ti.i0 + (PAIR ? (int)rank * 128 : 0) + ((!TN && !SWAP) ? ti.first : 0);
                 const int y_mn = ti.j0 + (PAIR ? (int)rank * T::Y_ROWS : 0) + (SWAP ? ti.first : 0);
                 const int red0 = TN ? ti.first : 0;
@@ -295,8 +316,6 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     if (tail) {
                         // counted by each CTA for itself: warp 2 clears the
                         // rows of other segments before the MMAs read them
-                        if (leader)
-                            mbar_arrive(&full[s]);
                         mbar_arrive_expect_tx(&tail_full[s], T::STAGE_BYTES);
                         const uint32_t bar = smem_addr(&tail_full[s]);
                         ragged_load<T::X_MN, false, false, 128>(dst, &tmap_x, bar, x_mn, red, ti.g);
@@ -311,6 +330,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         ragged_load<T::Y_MN, !TN && !SWAP, PAIR, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn, red,
                                                                            ti.g);
                         plain |= 1u << s;
+                        uses ^= 1u << s;
                     }
                     ++it;
                     if (++s == stages) {
@@ -325,7 +345,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 const uint32_t n = it < stages ? it : stages;
                 for (uint32_t i = it - n; i < it; ++i)
                     if ((plain >> (i % stages)) & 1u)
-                        drain_ragged(&full[i % stages], (i / stages) & 1, abort_flag, p);
+                        drain_ragged(&full[i % stages], ((uses >> (i % stages)) & 1) ^ 1, abort_flag, p);
             }
         }
     } else if (warp == 1) {
@@ -336,10 +356,11 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             const uint64_t y0 = ragged_desc<T::Y_MN>(base + T::X_BYTES);
             constexpr uint32_t X_STEP = (T::X_MN ? 2048u : 32u) >> 4; // 16 along the reduction
             constexpr uint32_t Y_STEP = (T::Y_MN ? 2048u : 32u) >> 4;
-            uint32_t s = 0, phase = 0, tile_it = 0, tail_phase = 0;
+            uint32_t s = 0, phase = 0, tile_it = 0;
+            uint32_t full_phase = 0, tail_phase = 0; // TN: per stage
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
                 if (ti.nkb == 0)
                     continue;
                 const uint32_t buf = tile_it & 1;
@@ -347,18 +368,24 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     break;
                 const uint32_t d = tmem_base + buf * (uint32_t)BN;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
-                    if (!wait_ragged(&full[s], phase, abort_flag, p)) {
-                        ok = false;
-                        break;
-                    }
                     int steps = RAGGED_BK / 16;
-                    if (TN && ti.rows - kb * RAGGED_BK < RAGGED_BK) {
-                        if (!wait_ragged(&tail_ready[s], (tail_phase >> s) & 1, abort_flag, p)) {
+                    if constexpr (TN) {
+                        // a segment's last block is announced by warp 2
+                        const bool tail = ti.rows - kb * RAGGED_BK < RAGGED_BK;
+                        if (!wait_ragged(tail ? &tail_ready[s] : &full[s],
+                                         ((tail ? tail_phase : full_phase) >> s) & 1, abort_flag, p)) {
                             ok = false;
                             break;
                         }
-                        tail_phase ^= 1u << s;
-                        steps = (ti.rows - kb * RAGGED_BK + 15) / 16;
+                        if (tail) {
+                            tail_phase ^= 1u << s;
+                            steps = (ti.rows - kb * RAGGED_BK + 15) / 16;
+                        } else {
+                            full_phase ^= 1u << s;
+                        }
+                    } else if (!wait_ragged(&full[s], phase, abort_flag, p)) {
+                        ok = false;
+                        break;
                     }
                     tc_fence_after();
                     const uint64_t xd = x0 + s * (T::STAGE_BYTES >> 4);
@@ -401,12 +428,14 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             uint32_t s = 0, tail_phase = 0;
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
-                s = (s + (uint32_t)ti.nkb) % stages;
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
+                s += (uint32_t)ti.nkb;
+                while (s >= stages)
+                    s -= stages;
                 const int valid = ti.rows & (RAGGED_BK - 1);
                 if (valid == 0)
                     continue;
-                const uint32_t st = (s + stages - 1) % stages; // the segment's last block
+                const uint32_t st = s == 0 ? stages - 1 : s - 1; // the segment's last block
                 bool got = wait_ragged(&tail_full[st], (tail_phase >> st) & 1, abort_flag, p);
                 if (!got) // aborting: an issued copy still lands before the CTA exits
                     drain_ragged(&tail_full[st], (tail_phase >> st) & 1, abort_flag, p);
@@ -444,7 +473,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         const bool bf16 = p.out_type == RAGGED_OUT_BF16;
         uint32_t tile_it = 0, slot = 0;
         for (int t = t_first; t < num_tiles; t += t_stride) {
-            const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, tiles, first, count);
+            const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
             const bool zero = ti.nkb == 0; // TN: a group without rows
             if (zero && p.accumulate)
                 continue;
@@ -464,20 +493,16 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 const int tok = min(NC, ti.rows - ti.j0 - c_first);
                 uint16_t *dst =
                     static_cast<uint16_t *>(p.d) + (size_t)(ti.first + ti.j0 + c_first) * p.d_cols + col;
-                constexpr int W = NC < 32 ? NC : 32;
 #pragma unroll
-                for (int c = 0; c < NC; c += W) {
+                for (int c = 0; c < NC; c += 32) {
                     if (c >= tok)
                         break;
-                    float v[W];
-                    if constexpr (W == 16)
-                        tmem_ld16(taddr + c, v);
-                    else
-                        tmem_ld32(taddr + c, v);
+                    float v[32];
+                    tmem_ld32(taddr + c, v);
                     tmem_wait_ld(v);
                     if (col < p.d_cols) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j)
+                        for (int j = 0; j < 32; ++j)
                             if (c + j < tok)
                                 dst[(size_t)(c + j) * p.d_cols] = (uint16_t)pack_16x2(v[j], 0.0f, bf16);
                     }
@@ -508,9 +533,23 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             const bool f32 = TN && p.out_type == RAGGED_OUT_F32;
             const int row = TN ? i0 : ti.first + i0;
             const int width = f32 ? 32 : 64; // columns per 128-byte staged row
+            // columns of this warp that exist
+            const int c_end = TN && row >= p.d_rows ? 0 : min(NC, p.d_cols - ti.j0 - c_first);
 #pragma unroll 1
             for (int c = 0; c < NC; c += 64) {
                 float v[2][32];
+                if (c >= c_end) {
+                    if (!zero && c + 64 >= NC) {
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR && !leader)
+                                mbar_arrive_cluster(map_shared_rank(smem_addr(&acc_empty[buf]), 0u));
+                            else
+                                mbar_arrive(&acc_empty[buf]);
+                        }
+                    }
+                    continue;
+                }
                 if (zero) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)

@@ -17,6 +17,23 @@ constexpr int RAGGED_MAX_STAGES = 12;
 constexpr int RAGGED_MAX_GROUPS = 1024;
 constexpr uint32_t RAGGED_SLOT_BYTES = 4096; // output staging: 32 rows of 128 bytes
 
+// Unsigned division by a constant for n < 2^31: q = (umulhi(n, mul) + n) >> shift
+// (Granlund and Montgomery's method).
+struct FastDiv {
+    uint32_t d, mul, shift;
+};
+
+inline FastDiv make_fast_div(uint32_t d)
+{
+    FastDiv f;
+    f.d = d;
+    f.shift = 0;
+    while ((1ull << f.shift) < d)
+        ++f.shift;
+    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+    return f;
+}
+
 struct RaggedParams {
     const int *offsets; // [num_groups + 1] segment bounds
     void *d;
@@ -29,7 +46,9 @@ struct RaggedParams {
     int nkb;             // NT, NN: 64-wide blocks of the reduction
     int x_blocks;        // SWAP: blocks of 128 output columns; TN: blocks of X rows
     int y_blocks;        // NT, NN without SWAP: blocks of output columns; TN: blocks of Y rows
-    int tiles_per_group; // TN
+    FastDiv tiles_per_group; // TN
+    FastDiv band;        // without SWAP: tiles of 8 X blocks; with it: token blocks take the slow way
+    FastDiv last_band;   // TN: X blocks of the last band
     int out_type;        // RaggedOut
     int accumulate;      // TN into FP32: add to the result
     uint32_t idesc;      // tcgen05.mma instruction descriptor

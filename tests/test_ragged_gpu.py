@@ -17,9 +17,9 @@ import fp8_fine_grained_nt_b200 as fp8
 
 pytestmark = pytest.mark.gpu
 
-FORMS = {"auto": (0, 0, 0), "swap32": (1, 0, 32), "swap64": (1, 0, 64), "swap128": (1, 0, 128),
+FORMS = {"auto": (0, 0, 0), "swap64": (1, 0, 64), "swap128": (1, 0, 128),
          "single": (0, 0, 256), "pair": (0, 1, 256)}
-TN_FORMS = {"auto": (0, 0, 0), "single": (0, 0, 128), "pair": (0, 1, 256)}
+TN_FORMS = {"auto": (0, 0, 0), "single128": (0, 0, 128), "single256": (0, 0, 256), "pair": (0, 1, 256)}
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
 
 # rows per group: empty, one, tile edges and beyond
@@ -172,7 +172,7 @@ def test_special_values_reach_their_rows_only():
     a[5, 7] = float("nan")
     a[41, 0] = float("inf")
     b[2, 9, 3] = float("inf")
-    for f in (FORMS["swap32"], FORMS["pair"]):
+    for f in (FORMS["swap64"], FORMS["pair"]):
         try:
             fp8.force_ragged(*f)
             d = torch.empty(T, 136, dtype=BF16, device="cuda")
