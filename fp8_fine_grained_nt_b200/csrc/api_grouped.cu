@@ -37,23 +37,27 @@ constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, wit
 
 // Time of a call in us by a wave model of the tile forms, with the mean rows per
 // group (the host does not know more) and counts spread evenly from none to
-// twice the mean.  Its constants were fitted to 98 calls on B200 (2 to 1024
-// rows per group, 8 to 64 groups, three sizes of weights, every form); the
-// form it takes is on average 1.2 % and at most 19 % slower than the best.
-// Some of them, us:
-//                                              swapped 64 / 128  128x256  pair
-//   NT 16 groups, N=4096, K=7168, 8 rows each        160 / 165      149    179
-//                                64 rows             228 / 173      158    199
-//                               512 rows            1102 / 646      516    472
-//   NN  8 groups, N=7168, K=2048, 8 rows              45 /  45       61     47
-//   NN 64 groups, N=2112, K=2048, 16 rows             87 /  91       93    105
-//                                                    128x128  128x256  pair
-//   TN 64 groups, N=2048, K=520, 64 rows                43       46       48
-//                              1024 rows               259      229      190
-//   TN  8 groups, N=7168, K=2048, 16 rows               53       46       49
+// twice the mean.  Back to back, these calls run under the power limit (1.2 to
+// 1.7 GHz), so the products that a form issues for padding rows cost time even
+// where memory bounds the call.  The constants were fitted to calls measured
+// that way on B200 (2 to 256 rows per group in 8 to 64 groups for NT and NN,
+// every form; the form taken is 1 % slower than the best on average, 20 % at
+// most) and, for TN, to 18 calls of 16 to 1024 rows per group (1 %, 8 %).
+// Some of them, us (SWAP by BN):
+//                                           16   32   64  128  128x256  pair
+//   NT 16 groups, N=4096, K=7168,  8 rows  157  166  174  187      169   213
+//                                 64 rows  621  333  253  211      186   252
+//                                256 rows             626  464     361   362
+//   NN  8 groups, N=7168, K=2048, 16 rows   78   42   45   48       61    57
+//                                128 rows       151  116   87       73    70
+//   NN 64 groups, N=2112, K=2048, 16 rows  128   96  103  116      107   142
+//                                          128x128  128x256  pair
+//   TN 64 groups, N=2048, K=520, 64 rows        43       46    48
+//                              1024 rows       259      229   190
+//   TN  8 groups, N=7168, K=2048, 16 rows       53       46    49
 double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K, int sms)
 {
-    const double cycles_per_us = 1900.0, bytes_per_us = 7.0e6;
+    const double cycles_per_us = 1900.0, bytes_per_us = 6.7e6;
     const double used = groups < rows ? groups : rows, mean = (double)rows / used;
     const double units = k.pair ? (sms > 1 ? sms / 2 : 1) : sms;
     const int bm = k.pair ? 256 : 128;
@@ -72,13 +76,15 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
     const double block = k.swap ? k.bn : bm, wide = k.swap ? 128 : k.bn;
     const double tok = 2 * mean <= block ? 1.0 : mean / block + 0.5; // token blocks of a group
     const double tiles = ceil(used * tok * ceil(out / wide));
-    const double mma = k.swap ? 2.0 * k.bn + 11.0 : 523.0, load = stage / 47.0;
-    const double tile = (ceil(red / 64.0) * (mma > load ? mma : load) + 1630.0) / cycles_per_us;
+    const double blocks = ceil(red / 64.0);
+    const double mma = (k.swap ? 2.0 * (k.bn < 32 ? 32 : k.bn) : 512.0) + 425.0, load = stage / 44.0;
+    const double tile = (blocks * (mma > load ? mma : load) + 4790.0) / cycles_per_us;
     const double weights = 2.0 * wide * red / tok / bytes_per_us; // read from memory for one tile
+    const double power = 2.0 * tiles * bm * k.bn * blocks * 64.0 / 1.96e10; // all products, padding too
     const double full = floor(tiles / units), rest = tiles - full * units;
     const double wave = tile > units * weights ? tile : units * weights;
     const double last = rest <= 0 ? 0 : tile > rest * weights ? tile : rest * weights;
-    return full * wave + last;
+    return full * wave + last + power;
 }
 
 // The kernel of a call.

@@ -493,16 +493,22 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 const int tok = min(NC, ti.rows - ti.j0 - c_first);
                 uint16_t *dst =
                     static_cast<uint16_t *>(p.d) + (size_t)(ti.first + ti.j0 + c_first) * p.d_cols + col;
+                constexpr int W = NC < 32 ? NC : 32;
 #pragma unroll
-                for (int c = 0; c < NC; c += 32) {
+                for (int c = 0; c < NC; c += W) {
                     if (c >= tok)
                         break;
-                    float v[32];
-                    tmem_ld32(taddr + c, v);
+                    float v[W < 16 ? 16 : W];
+                    if constexpr (W == 8)
+                        tmem_ld8(taddr + c, v);
+                    else if constexpr (W == 16)
+                        tmem_ld16(taddr + c, v);
+                    else
+                        tmem_ld32(taddr + c, v);
                     tmem_wait_ld(v);
                     if (col < p.d_cols) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < W; ++j)
                             if (c + j < tok)
                                 dst[(size_t)(c + j) * p.d_cols] = (uint16_t)pack_16x2(v[j], 0.0f, bf16);
                     }

@@ -17,7 +17,7 @@ import fp8_fine_grained_nt_b200 as fp8
 
 pytestmark = pytest.mark.gpu
 
-FORMS = {"auto": (0, 0, 0), "swap64": (1, 0, 64), "swap128": (1, 0, 128),
+FORMS = {"auto": (0, 0, 0), "swap16": (1, 0, 16), "swap32": (1, 0, 32), "swap64": (1, 0, 64), "swap128": (1, 0, 128),
          "single": (0, 0, 256), "pair": (0, 1, 256)}
 TN_FORMS = {"auto": (0, 0, 0), "single128": (0, 0, 128), "single256": (0, 0, 256), "pair": (0, 1, 256)}
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
