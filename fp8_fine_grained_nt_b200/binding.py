@@ -267,6 +267,10 @@ _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _HALF = (torch.bfloat16, torch.float16)
 
 
+# The checks below run on every call of operators that take a few microseconds
+# on the GPU, so they ask each tensor for as little as they can.
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     """Index of the CUDA device that `t` is on."""
     if not isinstance(t, torch.Tensor):
@@ -277,19 +281,32 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     return index
 
 
-def _arg(t: torch.Tensor, name: str, dtype, ndim: int, device: int, dense: bool = True) -> int:
-    """Checked pointer of a tensor on `device` (`dense`: contiguous; else only its rows are)."""
+def _arg(t: torch.Tensor, name: str, dtype, ndim: int, device: int) -> int:
+    """Checked pointer of a contiguous tensor on `device`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.dim() == ndim \
+            and t.is_contiguous():
+        return t.data_ptr()
+    raise _refusal(t, name, dtype, ndim, device, "must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device: int) -> int:
+    """Checked pointer of a matrix on `device` whose rows are contiguous."""
+    if isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.dim() == 2 \
+            and (t.is_contiguous() or t.stride(1) == 1 or t.size(1) == 1):
+        return t.data_ptr()
+    raise _refusal(t, name, dtype, 2, device, "must have contiguous rows")
+
+
+def _refusal(t, name: str, dtype, ndim: int, device: int, layout: str) -> Exception:
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+        return TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}, not on {t.device}")
+        return ValueError(f"{name} must be a CUDA tensor on cuda:{device}, not on {t.device}")
     if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        return TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    if not t.is_contiguous() and (dense or (t.size(1) > 1 and t.stride(1) != 1)):
-        raise ValueError(f"{name} must be contiguous" if dense else f"{name} must have contiguous rows")
-    return t.data_ptr()
+        return ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    return ValueError(f"{name} {layout}")
 
 
 def _half(t: torch.Tensor, name: str):
@@ -308,7 +325,7 @@ def _call(name: str, stream, device: int, *args) -> None:
     else:
         raw = stream.cuda_stream
     fn = getattr(_lib or load_library(), name)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -373,7 +390,7 @@ def k_grouped_gemm_tn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
     return d
 
 
-def _workspace(given, need: int, stream, device: int):
+def _workspace(given, need: int, stream, device: int, like: torch.Tensor):
     """(pointer, bytes, owner) of the caller's workspace, or of one from torch's
     allocator that belongs to the stream the call runs on."""
     if given is not None:
@@ -383,10 +400,10 @@ def _workspace(given, need: int, stream, device: int):
     if need == 0:
         return 0, 0, None
     if stream is None:
-        own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
+        own = like.new_empty(need, dtype=torch.uint8)
     else:
         with torch.cuda.stream(stream):
-            own = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
+            own = like.new_empty(need, dtype=torch.uint8)
     return own.data_ptr(), need, own
 
 
@@ -433,7 +450,7 @@ def group_rows_by_index(index: torch.Tensor, num_groups: int, offsets: torch.Ten
     if (offsets.size(0) != num_groups + 1 or order.size(0) != cap or (slots is not None and slots.size(0) != R)
             or (m_indices is not None and m_indices.size(0) != cap)):
         raise ValueError(f"offsets must hold {num_groups + 1} values, order and m_indices {cap}, slots {R}")
-    ptr, size, _own = _workspace(workspace, _size("get_group_rows_workspace_size", R, num_groups), stream, device)
+    ptr, size, _own = _workspace(workspace, _size("get_group_rows_workspace_size", R, num_groups), stream, device, index)
     _call("group_rows_by_index", stream, device, *args, R, num_groups, alignment, ptr, size)
     return offsets, order, slots, m_indices
 
@@ -466,14 +483,14 @@ def m_grouped_lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tens
     if order is None and S > T:
         raise ValueError(f"m_indices holds {S} slots for {T} rows")
     device, dtype = _device_of(x, "x"), _half(x, "x")
-    args = (_arg(x, "x", dtype, 2, device, False), x.stride(0) if T > 1 else K,
+    args = (_rows(x, "x", dtype, device), x.stride(0) if T > 1 else K,
             _arg(lora_a, "lora_a", dtype, 3, device), _arg(lora_b, "lora_b", dtype, 3, device),
             _arg(scales, "scales", torch.float32, 1, device),
-            _arg(c, "c", dtype, 2, device, False), c.stride(0) if T > 1 else N,
-            _arg(d, "d", dtype, 2, device, False), d.stride(0) if T > 1 else N,
+            _rows(c, "c", dtype, device), c.stride(0) if T > 1 else N,
+            _rows(d, "d", dtype, device), d.stride(0) if T > 1 else N,
             _arg(m_indices, "m_indices", torch.int32, 1, device),
             None if order is None else _arg(order, "order", torch.int32, 1, device))
-    ptr, size, _own = _workspace(workspace, _size("get_lora_workspace_size", S, L, R, N, K), stream, device)
+    ptr, size, _own = _workspace(workspace, _size("get_lora_workspace_size", S, L, R, N, K), stream, device, x)
     _call("m_grouped_lora_add", stream, device, *args, _DTYPE_CODE[dtype], S, T, L, R, N, K, ptr, size)
     return d
 
