@@ -4,7 +4,10 @@ Argument marshalling only: each call checks dtypes, devices and shapes, passes
 raw device pointers, sizes and the current CUDA stream to the library, and
 raises ``Fp8NtError`` on a nonzero status.  Every step of the GEMM runs in the
 library's kernels.  The library is loaded on first use; if it is missing or
-fails to load, the call raises (there is no fallback).
+fails to load, the call raises (there is no fallback).  The grouped operators,
+which may take a few microseconds on the GPU, go through the extension module
+``_torch_calls``, which makes the same checks faster; a call that fails one (or
+names a stream, a workspace or another device) comes back to the code here.
 """
 
 from __future__ import annotations
@@ -57,6 +60,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libfp8nt.so"
 _lock = threading.Lock()
 _lib = None
+_calls = None  # the extension module
 
 KIND_DENSE, KIND_CONTIGUOUS, KIND_MASKED, KIND_DENSE_PER_TENSOR = 0, 1, 2, 3
 
@@ -127,6 +131,19 @@ def load_library():
         lib.dg_force_ragged.argtypes = [I, I, I]
         _lib = lib
         return lib
+
+
+def _load_calls():
+    """Load the extension module beside libfp8nt.so (raises if it has not been built)."""
+    global _calls
+    load_library()  # first: it is the library the module is linked to
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise ImportError("_torch_calls.so is missing or does not fit this torch: build it with "
+                          "`python -m fp8_fine_grained_nt_b200.build`") from e
+    _calls = _torch_calls
+    return _torch_calls
 
 
 def status_string(status: int) -> str:
@@ -350,6 +367,12 @@ def m_grouped_gemm_nt_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
     int32 on the device, segment g being rows offsets[g] to offsets[g+1] (any
     length, no padding).  Rows outside every segment are left as they are.
     """
+    if stream is None:
+        status = (_calls or _load_calls()).m_grouped_gemm_nt_ragged(a, b, d, offsets)
+        if status == 0:
+            return d
+        if status > 0:
+            raise Fp8NtError(status, "m_grouped_gemm_nt_ragged")
     G, N, K = b.shape
     if a.shape[1] != K or tuple(d.shape) != (a.shape[0], N) or offsets.shape[0] != G + 1:
         raise ValueError("shape mismatch between a, b, d and offsets")
@@ -363,6 +386,12 @@ def m_grouped_gemm_nn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
     a: [T,N] (gradients of the forward's output); b: [G,N,K] (the forward's
     weights, not transposed); d: [T,K]; offsets as in the forward.
     """
+    if stream is None:
+        status = (_calls or _load_calls()).m_grouped_gemm_nn_ragged(a, b, d, offsets)
+        if status == 0:
+            return d
+        if status > 0:
+            raise Fp8NtError(status, "m_grouped_gemm_nn_ragged")
     G, N, K = b.shape
     if a.shape[1] != N or tuple(d.shape) != (a.shape[0], K) or offsets.shape[0] != G + 1:
         raise ValueError("shape mismatch between a, b, d and offsets")
@@ -378,6 +407,12 @@ def k_grouped_gemm_tn_ragged(a: torch.Tensor, b: torch.Tensor, d: torch.Tensor,
     input), both bf16 or fp16; d: [G,N,K] fp32 or their type.  accumulate: add to
     d (fp32 only), else d is written in full (zeros for a group without rows).
     """
+    if stream is None:
+        status = (_calls or _load_calls()).k_grouped_gemm_tn_ragged(a, b, d, offsets, accumulate)
+        if status == 0:
+            return d
+        if status > 0:
+            raise Fp8NtError(status, "k_grouped_gemm_tn_ragged")
     G, N, K = d.shape
     if a.shape[1] != N or b.shape[1] != K or a.shape[0] != b.shape[0] or offsets.shape[0] != G + 1:
         raise ValueError("shape mismatch between a, b, d and offsets")
@@ -438,6 +473,13 @@ def group_rows_by_index(index: torch.Tensor, num_groups: int, offsets: torch.Ten
     -1 (optional); capacity = get_row_groups_capacity(R, num_groups, alignment).
     Returns (offsets, order, slots, m_indices).
     """
+    if stream is None and workspace is None:
+        status = (_calls or _load_calls()).group_rows_by_index(index, num_groups, offsets, order, slots, m_indices,
+                                                               alignment)
+        if status == 0:
+            return offsets, order, slots, m_indices
+        if status > 0:
+            raise Fp8NtError(status, "group_rows_by_index")
     device = _device_of(index, "index")
     if index.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"index has dtype {index.dtype}, expected int32 or int64")
@@ -474,6 +516,12 @@ def m_grouped_lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tens
     slot with an adapter are not written.  Slots sorted by adapter
     (group_rows_by_index) share the reads of its weights.
     """
+    if stream is None and workspace is None:
+        status = (_calls or _load_calls()).m_grouped_lora_add(x, lora_a, lora_b, scales, c, d, m_indices, order)
+        if status == 0:
+            return d
+        if status > 0:
+            raise Fp8NtError(status, "m_grouped_lora_add")
     L, R, K = lora_a.shape
     T, N = d.shape
     S = m_indices.size(0)

@@ -1,4 +1,5 @@
-"""Build libfp8nt.so in-tree with nvcc for sm_100a (ahead of time, no JIT).
+"""Build libfp8nt.so in-tree with nvcc for sm_100a (ahead of time, no JIT), and
+_torch_calls.so, the extension module that calls it, with the host compiler.
 
 Compiles csrc/api.cu and one object per kernel shape listed in
 csrc/kernels.def (csrc/instance.cu with -DFP8NT_MW / -DFP8NT_BN / -DFP8NT_PAIR / -DFP8NT_SCALAR)
@@ -17,6 +18,7 @@ from __future__ import annotations
 
 import argparse
 import hashlib
+import importlib.metadata
 import os
 import re
 import shutil
@@ -29,6 +31,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libfp8nt.so")
+CALLS_PATH = os.path.join(HERE, "_torch_calls.so")
 REGS_AT_LAUNCH = 168
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -124,7 +127,7 @@ def _check_ptxas(report: str, what: str) -> list[str]:
             current = m.group(1)
             continue
         m = re.search(r"Used (\d+) registers", line)
-        if m and current and "fp8_gemm_kernel" in current:
+        if m and current and ("fp8_gemm_kernel" in current or "ragged_kernelILi3E" in current):
             regs = int(m.group(1))
             if regs != REGS_AT_LAUNCH:
                 raise RuntimeError(f"{what}: kernel uses {regs} registers at launch, the "
@@ -137,9 +140,10 @@ def _check_ptxas(report: str, what: str) -> list[str]:
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    digest = _sources_digest([])
+    # (the extension module belongs to one Python and one torch)
+    digest = f"{_sources_digest([])} {sys.version_info[:2]} {importlib.metadata.version('torch')}"
     stamp = os.path.join(BUILD_DIR, "libfp8nt.digest")
-    if (not force and os.path.exists(LIB_PATH) and os.path.exists(stamp)
+    if (not force and os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH) and os.path.exists(stamp)
             and open(stamp).read() == digest):
         return LIB_PATH
     jobs = jobs or max(1, os.cpu_count() or 1)
@@ -176,9 +180,32 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     if proc.returncode != 0:
         raise RuntimeError(f"link failed:\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, LIB_PATH)
+    _build_calls()
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB_PATH
+
+
+def _build_calls() -> None:
+    """csrc/torch_calls.cpp, the extension module binding.py calls the grouped
+    operators through (against the installed torch's headers, linked to
+    libfp8nt.so beside it)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
+           f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "torch_calls.cpp"),
+           "-o", tmp, f"-L{HERE}", "-l:libfp8nt.so", "-Wl,-rpath,$ORIGIN", f"-L{root}/lib", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"torch_calls.cpp failed:\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def main():

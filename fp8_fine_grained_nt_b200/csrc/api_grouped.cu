@@ -62,14 +62,14 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
     const double units = k.pair ? (sms > 1 ? sms / 2 : 1) : sms;
     const int bm = k.pair ? 256 : 128;
     const double stage = 16384.0 + 128.0 * (k.pair ? k.bn / 2 : k.bn);
-    if (k.dir == RAGGED_TN) {
+    if (k.dir == RAGGED_TN || k.dir == RAGGED_TN32) {
         // a tile: its blocks of 64 rows, or its epilogue, whichever is longer
         const double tiles = (double)groups * ceil_div(N, bm) * ceil_div(K, k.bn);
         const double mma = 2.0 * k.bn + 580.0, load = stage / 39.0;
         const double blocks = ceil(mean / 64.0) * (mma > load ? mma : load) + 1100.0;
         const double epilogue = 700.0 + 1450.0 * k.bn / 128.0;
         const double busy = ceil(tiles / units) * (blocks > epilogue ? blocks : epilogue) / cycles_per_us;
-        const double memory = (2.0 * groups * N * K + 2.0 * rows * ((double)N + K)) / bytes_per_us;
+        const double memory = ((k.dir == RAGGED_TN32 ? 4.0 : 2.0) * groups * N * K + 2.0 * rows * ((double)N + K)) / bytes_per_us;
         return busy > memory ? busy : memory;
     }
     const double out = k.dir == RAGGED_NT ? N : K, red = k.dir == RAGGED_NT ? K : N;
@@ -143,13 +143,14 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     int st = current_device(&dev);
     if (st != DG_OK)
         return st;
-    const bool tn = dir == RAGGED_TN;
+    const bool tn = dir == RAGGED_TN || dir == RAGGED_TN32;
     if (M_sum == 0) { // the weight gradient of no rows
         if (accumulate)
             return DG_OK;
         const size_t bytes = (size_t)G * N * K * (d_type == RAGGED_OUT_F32 ? 4 : 2);
         return cudaMemsetAsync(D, 0, bytes, stream) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
     }
+    // the result's type picks the kernel of a weight gradient
     const RaggedKernel *k = choose_ragged(dir, G, M_sum, N, K, dev.sms);
     if (!k)
         return DG_ERR_UNSUPPORTED_SHAPE;
@@ -297,7 +298,7 @@ int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *o
     // that a sum over many calls is not rounded to 16 bits at each
     if ((d_dtype != DG_INPUT_F32 && d_dtype != dtype) || (accumulate && d_dtype != DG_INPUT_F32))
         return DG_ERR_INVALID_ARGUMENT;
-    return run_ragged(RAGGED_TN, A, B, D, offsets, dtype, d_dtype, accumulate != 0, num_groups, M_sum, N, K,
+    return run_ragged(d_dtype == DG_INPUT_F32 ? RAGGED_TN32 : RAGGED_TN, A, B, D, offsets, dtype, d_dtype, accumulate != 0, num_groups, M_sum, N, K,
                       reinterpret_cast<cudaStream_t>(stream));
 }
 

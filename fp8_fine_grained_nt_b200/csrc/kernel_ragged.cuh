@@ -11,7 +11,12 @@
 // with i / j contiguous ("MN-major"), so no operand is ever transposed in
 // memory: NT reads both K-major, NN reads b MN-major, TN reads both MN-major.
 // Accumulation is FP32 in tensor memory over the whole reduction; the result
-// is rounded once, on store.
+// is rounded once, on store.  The tensor core rounds each step of 16 towards
+// zero, a bias that grows with the length: nothing beside the rounding to 16
+// bits, but 4e-6 of an FP32 weight gradient over 2048 rows (and 3e-5 over
+// 16384).  So FP32 results (direction TN32) are added up in registers, rounded
+// to nearest, from partial sums of 512 rows: 5e-7, for 7 % of the time (477 -> 510 us at 16384
+// rows, N = 7168, K = 2048; partial sums of 256 rows cost 15 %).
 //
 // Tile forms:
 //   PAIR   256 x 256 by a cluster of two CTAs (cta_group::2): each CTA loads
@@ -39,12 +44,13 @@ namespace fp8nt {
 template <int DIR, bool SWAP, bool PAIR, int BN>
 struct RaggedTraits {
     static_assert(!PAIR || (BN == 256 && !SWAP), "a CTA pair computes 256 x 256");
-    static_assert(DIR != RAGGED_TN || !SWAP, "the weight gradient has no swapped form");
+    static constexpr bool TN = DIR == RAGGED_TN || DIR == RAGGED_TN32;
+    static_assert(!TN || !SWAP, "the weight gradient has no swapped form");
     static constexpr int BM = PAIR ? 256 : 128;      // rows of X per tile
     static constexpr int Y_ROWS = PAIR ? BN / 2 : BN; // rows of Y each CTA loads
     // a side is MN-major where its i / j index is the contiguous one in memory
-    static constexpr bool X_MN = DIR == RAGGED_TN || (DIR == RAGGED_NN && SWAP);
-    static constexpr bool Y_MN = DIR == RAGGED_TN || (DIR == RAGGED_NN && !SWAP);
+    static constexpr bool X_MN = TN || (DIR == RAGGED_NN && SWAP);
+    static constexpr bool Y_MN = TN || (DIR == RAGGED_NN && !SWAP);
     static_assert(!Y_MN || Y_ROWS % 64 == 0, "MN-major operands load in 64-wide chunks");
     static constexpr uint32_t X_BYTES = 128 * 128;
     static constexpr uint32_t Y_BYTES = Y_ROWS * 128;
@@ -77,9 +83,10 @@ template <int DIR, bool SWAP, int BM, int BN>
 __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, int &g, const int *tiles,
                                                   const int *first, const int *count)
 {
+    constexpr bool TN = DIR == RAGGED_TN || DIR == RAGGED_TN32;
     RaggedTile r;
     int local, xb, yb;
-    if (DIR == RAGGED_TN) {
+    if (TN) {
         g = fast_div(t, p.tiles_per_group);
         local = t - g * (int)p.tiles_per_group.d;
         xb = p.x_blocks;
@@ -115,14 +122,14 @@ __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, 
         int y;
         if (width >= 8)
             y = in_band >> 3;
-        else if (DIR == RAGGED_TN)
+        else if (TN)
             y = fast_div(in_band, p.last_band);
         else
             y = in_band / width;
         r.i0 = (band * 8 + in_band - y * min(width, 8)) * BM;
         r.j0 = y * BN;
     }
-    r.nkb = DIR == RAGGED_TN ? (r.rows + RAGGED_BK - 1) / RAGGED_BK : p.nkb;
+    r.nkb = TN ? (r.rows + RAGGED_BK - 1) / RAGGED_BK : p.nkb;
     return r;
 }
 
@@ -182,7 +189,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                   const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ RaggedParams p)
 {
     using T = RaggedTraits<DIR, SWAP, PAIR, BN>;
-    constexpr bool TN = DIR == RAGGED_TN;
+    constexpr bool TN = T::TN;
+    constexpr bool F32 = DIR == RAGGED_TN32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -294,6 +302,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        if constexpr (F32)
+            regs_dec<RAGGED_REGS_OTHER>();
         if (lane == 0) {
             uint32_t it = 0, s = 0, phase = 1;
             // per stage: its last use was counted on full[], and the parity of
@@ -350,6 +360,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
+        if constexpr (F32)
+            regs_dec<RAGGED_REGS_OTHER>();
         if (lane == 0 && leader) {
             const uint32_t base = smem_addr(smem);
             const uint64_t x0 = ragged_desc<T::X_MN>(base);
@@ -363,11 +375,20 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
                 if (ti.nkb == 0)
                     continue;
-                const uint32_t buf = tile_it & 1;
+                uint32_t buf = tile_it & 1;
                 if (!wait_ragged(&acc_empty[buf], ((tile_it >> 1) & 1) ^ 1, abort_flag, p))
                     break;
-                const uint32_t d = tmem_base + buf * (uint32_t)BN;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
+                    // FP32 results: a fresh accumulator for each partial sum
+                    if (F32 && kb > 0 && kb % RAGGED_PARTIAL == 0) {
+                        buf = ++tile_it & 1;
+                        if (!wait_ragged(&acc_empty[buf], ((tile_it >> 1) & 1) ^ 1, abort_flag, p)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    const uint32_t d = tmem_base + buf * (uint32_t)BN;
+                    const bool first_kb = F32 ? kb % RAGGED_PARTIAL == 0 : kb == 0;
                     int steps = RAGGED_BK / 16;
                     if constexpr (TN) {
                         // a segment's last block is announced by warp 2
@@ -393,12 +414,13 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < RAGGED_BK / 16; ++k)
                         if (!TN || k < steps)
-                            mma_f16<PAIR>(d, xd + k * X_STEP, yd + k * Y_STEP, p.idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                            mma_f16<PAIR>(d, xd + k * X_STEP, yd + k * Y_STEP, p.idesc,
+                                          (!first_kb || k > 0) ? 1u : 0u);
                     if constexpr (PAIR)
                         mma_commit_pair_mc(&empty[s], 0x3);
                     else
                         mma_commit(&empty[s]);
-                    if (kb == ti.nkb - 1) {
+                    if (kb == ti.nkb - 1 || (F32 && kb % RAGGED_PARTIAL == RAGGED_PARTIAL - 1)) {
                         if constexpr (PAIR)
                             mma_commit_pair_mc(&acc_full[buf], 0x3);
                         else
@@ -420,6 +442,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ segment ends (TN)
+        if constexpr (F32)
+            regs_dec<RAGGED_REGS_OTHER>();
         // The last block of a segment holds rows of the next one (or behind
         // the last): they are cleared in both operands, so that they count as
         // zero whatever they hold.  A reduction row is one 128-byte line per
@@ -462,8 +486,13 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        if constexpr (F32)
+            regs_dec<RAGGED_REGS_OTHER>();
+    } else {
         // ------------------------------------------------------------ epilogue
+        if constexpr (F32) // these warps hold the sums
+            regs_inc<RAGGED_REGS_EPILOGUE>();
         const int q = warp & 3;
         constexpr int NC = BN / 2; // columns of this warp, from c_first on
         const int c_first = warp >= 8 ? NC : 0;
@@ -477,6 +506,76 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             const bool zero = ti.nkb == 0; // TN: a group without rows
             if (zero && p.accumulate)
                 continue;
+            if constexpr (F32) {
+                // the tile's partial sums, added up in registers
+                float acc[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    acc[c] = 0.0f;
+                bool got = true;
+                for (int kb = 0; kb < ti.nkb; kb += RAGGED_PARTIAL, ++tile_it) {
+                    const uint32_t buf = tile_it & 1;
+                    got = wait_ragged(&acc_full[buf], (tile_it >> 1) & 1, abort_flag, p);
+                    got = __all_sync(0xffffffffu, got);
+                    if (!got)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < NC; c += 32) {
+                        float v[32];
+                        tmem_ld32(taddr0 + buf * (uint32_t)BN + c, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            acc[c + j] += v[j];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR && !leader)
+                            mbar_arrive_cluster(map_shared_rank(smem_addr(&acc_empty[buf]), 0u));
+                        else
+                            mbar_arrive(&acc_empty[buf]);
+                    }
+                }
+                if (!got)
+                    break;
+                const int row = ti.i0 + (PAIR ? (int)rank * 128 : 0) + q * 32;
+                if (row >= p.d_rows)
+                    continue;
+#pragma unroll
+                for (int c = 0; c < NC; c += 32) {
+                    const int col = ti.j0 + c_first + c;
+                    if (col >= p.d_cols)
+                        break;
+                    if (lane == 0) { // the slot's last store has read it
+                        if (p.out_slots == 2)
+                            bulk_wait_read_1();
+                        else
+                            bulk_wait_read_all();
+                    }
+                    __syncwarp();
+                    const uint32_t stg = stg_w + slot * RAGGED_SLOT_BYTES;
+                    // 16-byte piece i of row r sits at piece i ^ (r % 8): TMA's 128-byte swizzle
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_v4(stg + lane * 128 + ((i ^ (lane & 7)) << 4), __float_as_uint(acc[c + 4 * i]),
+                                     __float_as_uint(acc[c + 4 * i + 1]), __float_as_uint(acc[c + 4 * i + 2]),
+                                     __float_as_uint(acc[c + 4 * i + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (p.accumulate)
+                            tma_add_3d(&tmap_d, stg, col, row, ti.g);
+                        else
+                            tma_store_3d(&tmap_d, stg, col, row, ti.g);
+                        bulk_commit_group();
+                    }
+                    __syncwarp();
+                    slot = slot + 1 == (uint32_t)p.out_slots ? 0 : slot + 1;
+                }
+                continue;
+            }
             const uint32_t buf = tile_it & 1;
             if (!zero) {
                 const bool got = wait_ragged(&acc_full[buf], (tile_it >> 1) & 1, abort_flag, p);
@@ -536,9 +635,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 ++tile_it;
                 continue;
             }
-            const bool f32 = TN && p.out_type == RAGGED_OUT_F32;
             const int row = TN ? i0 : ti.first + i0;
-            const int width = f32 ? 32 : 64; // columns per 128-byte staged row
             // columns of this warp that exist
             const int c_end = TN && row >= p.d_rows ? 0 : min(NC, p.d_cols - ti.j0 - c_first);
 #pragma unroll 1
@@ -576,69 +673,50 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         }
                     }
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!f32 && h == 1)
-                        break;
-                    const int col = ti.j0 + c_first + c + h * 32;
-                    // the slot's last store has read it
-                    if (lane == 0) {
-                        if (p.out_slots == 2)
-                            bulk_wait_read_1();
-                        else
-                            bulk_wait_read_all();
-                    }
-                    __syncwarp();
-                    const uint32_t stg = stg_w + slot * RAGGED_SLOT_BYTES;
-                    const uint32_t line = stg + lane * 128;
-                    // 16-byte piece i of row r sits at piece i ^ (r % 8): TMA's 128-byte swizzle
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t at = line + ((i ^ (lane & 7)) << 4);
-                        if (f32) {
-                            st_shared_v4(at, __float_as_uint(v[h][4 * i]), __float_as_uint(v[h][4 * i + 1]),
-                                         __float_as_uint(v[h][4 * i + 2]), __float_as_uint(v[h][4 * i + 3]));
-                        } else {
-                            const float *w = &v[i >> 2][(i & 3) * 8];
-                            st_shared_v4(at, pack_16x2(w[0], w[1], bf16), pack_16x2(w[2], w[3], bf16),
-                                         pack_16x2(w[4], w[5], bf16), pack_16x2(w[6], w[7], bf16));
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (whole) {
-                        if (lane == 0) {
-                            if (col < p.d_cols && (!TN || row < p.d_rows)) {
-                                if constexpr (TN) {
-                                    if (p.accumulate)
-                                        tma_add_3d(&tmap_d, stg, col, row, ti.g);
-                                    else
-                                        tma_store_3d(&tmap_d, stg, col, row, ti.g);
-                                } else {
-                                    tma_store_2d(&tmap_d, stg, col, row);
-                                }
-                            }
-                            bulk_commit_group();
-                        }
-                    } else {
-                        // a segment's last rows: 8 lanes store a row's 128 bytes
-                        const int piece = lane & 7;
-#pragma unroll 1
-                        for (int r = lane >> 3; r < left; r += 4) {
-                            const uint4 w = ld_shared_v4(stg + r * 128 + ((piece ^ (r & 7)) << 4));
-                            if (col + piece * 8 < p.d_cols)
-                                st_global_v4(static_cast<uint16_t *>(p.d) + (size_t)(row + r) * p.d_cols + col +
-                                                 piece * 8,
-                                             w.x, w.y, w.z, w.w);
-                        }
-                        if (lane == 0)
-                            bulk_commit_group(); // empty: keeps one group per slot use
-                    }
-                    __syncwarp();
-                    slot = slot + 1 == (uint32_t)p.out_slots ? 0 : slot + 1;
-                    if (width == 64)
-                        break;
+                const int col = ti.j0 + c_first + c;
+                // the slot's last store has read it
+                if (lane == 0) {
+                    if (p.out_slots == 2)
+                        bulk_wait_read_1();
+                    else
+                        bulk_wait_read_all();
                 }
+                __syncwarp();
+                const uint32_t stg = stg_w + slot * RAGGED_SLOT_BYTES;
+                const uint32_t line = stg + lane * 128;
+                // 16-byte piece i of row r sits at piece i ^ (r % 8): TMA's 128-byte swizzle
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float *w = &v[i >> 2][(i & 3) * 8];
+                    st_shared_v4(line + ((i ^ (lane & 7)) << 4), pack_16x2(w[0], w[1], bf16),
+                                 pack_16x2(w[2], w[3], bf16), pack_16x2(w[4], w[5], bf16),
+                                 pack_16x2(w[6], w[7], bf16));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (whole) {
+                    if (lane == 0) {
+                        if constexpr (TN)
+                            tma_store_3d(&tmap_d, stg, col, row, ti.g);
+                        else
+                            tma_store_2d(&tmap_d, stg, col, row);
+                        bulk_commit_group();
+                    }
+                } else {
+                    // a segment's last rows: 8 lanes store a row's 128 bytes
+                    const int piece = lane & 7;
+#pragma unroll 1
+                    for (int r = lane >> 3; r < left; r += 4) {
+                        const uint4 w = ld_shared_v4(stg + r * 128 + ((piece ^ (r & 7)) << 4));
+                        if (col + piece * 8 < p.d_cols)
+                            st_global_v4(static_cast<uint16_t *>(p.d) + (size_t)(row + r) * p.d_cols + col + piece * 8,
+                                         w.x, w.y, w.z, w.w);
+                    }
+                    if (lane == 0)
+                        bulk_commit_group(); // empty: keeps one group per slot use
+                }
+                __syncwarp();
+                slot = slot + 1 == (uint32_t)p.out_slots ? 0 : slot + 1;
             }
             if (!zero)
                 ++tile_it;

@@ -8,11 +8,16 @@
 
 namespace fp8nt {
 
-enum RaggedDir : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2 };
+enum RaggedDir : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2, RAGGED_TN32 = 3 }; // TN32: FP32 result
 enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 = 2 };
 
 constexpr int RAGGED_BK = 64;           // reduction elements per stage: 128-byte swizzled rows
 constexpr int RAGGED_THREADS = 384;     // 12 warps, 8 of them in the epilogue
+constexpr int RAGGED_PARTIAL = 8;       // TN32: blocks of the reduction per partial sum
+constexpr int RAGGED_REGS_OTHER = 56;   // TN32: registers of warps 0-3 and of the epilogue warps
+constexpr int RAGGED_REGS_EPILOGUE = 224;
+static_assert(4 * 32 * RAGGED_REGS_OTHER + 8 * 32 * RAGGED_REGS_EPILOGUE <= RAGGED_THREADS * REGS_AT_LAUNCH,
+              "register split exceeds the launch allocation");
 constexpr int RAGGED_MAX_STAGES = 12;
 constexpr int RAGGED_MAX_GROUPS = 1024;
 constexpr uint32_t RAGGED_SLOT_BYTES = 4096; // output staging: 32 rows of 128 bytes
@@ -50,7 +55,7 @@ struct RaggedParams {
     FastDiv band;        // without SWAP: tiles of 8 X blocks; with it: token blocks take the slow way
     FastDiv last_band;   // TN: X blocks of the last band
     int out_type;        // RaggedOut
-    int accumulate;      // TN into FP32: add to the result
+    int accumulate;      // TN32: add to the result
     uint32_t idesc;      // tcgen05.mma instruction descriptor
     int stages;
     int out_slots;       // staging slots per epilogue warp (0 with SWAP)

@@ -150,6 +150,23 @@ def test_tn_sizes(N, K, dtype):
     run_tn([5, 0, 300, 40], N, K, dtype, FP32, seed=N - K)
 
 
+@pytest.mark.parametrize("name", list(TN_FORMS))
+@pytest.mark.parametrize("rows", [256, 2049, 20000])
+def test_tn_long_sums_in_fp32(name, rows, form):
+    """FP32 results hold their accuracy over long segments: a partial sum of 512
+    rows is 32 truncated steps, each off by half a step of 2^-23 of the sum so far
+    on average (so 32 / 2 * 2/3 * 2^-23 of the whole, 1.3e-6 at the very most and
+    half of that with the mantissas' spread), the errors of the partial sums add
+    up as the sums themselves do: within 2^-20 of the result."""
+    form(TN_FORMS[name])
+    offsets, ends, T = layout([rows, 3])
+    a, b = gen(T, 256, seed=1, dtype=BF16), gen(T, 264, seed=2, dtype=BF16)
+    d = torch.empty(2, 256, 264, dtype=FP32, device="cuda")
+    fp8.k_grouped_gemm_tn_ragged(a, b, d, offsets)
+    ref = a[:rows].double().T @ b[:rows].double()
+    assert (d[0].double() - ref).norm() <= 2.0 ** -20 * ref.norm()
+
+
 def test_tn_neighbours_do_not_leak():
     """A segment's last block reads the next segment's rows: Inf there stays there."""
     counts = [17, 30, 1, 64, 63]
