@@ -469,13 +469,12 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 }
                 tail_phase ^= 1u << st;
                 constexpr int CHUNKS = (int)(T::STAGE_BYTES / 8192);
-                const int clear = ((valid + 15) & ~15) - valid;
-                const uint32_t base = smem_addr(smem) + st * T::STAGE_BYTES;
-                for (int i = lane; i < CHUNKS * clear * 8; i += 32) {
-                    const int piece = i & 7, line = i >> 3;
-                    const int c = line / clear, r = valid + line % clear;
-                    st_shared_v4(base + c * 8192 + r * 128 + piece * 16, 0u, 0u, 0u, 0u);
-                }
+                const int end = (valid + 15) & ~15; // the MMAs' steps of 16 end here
+                const uint32_t at = smem_addr(smem) + st * T::STAGE_BYTES + (lane & 7) * 16;
+                for (int r = valid + (lane >> 3); r < end; r += 4)
+#pragma unroll
+                    for (int c = 0; c < CHUNKS; ++c)
+                        st_shared_v4(at + c * 8192 + r * 128, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
