@@ -173,7 +173,8 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     const int red = dir == RAGGED_NT ? K : N; // reduction of NT, NN
     p.d_rows = N;
     p.d_cols = out;
-    p.nkb = (int)ceil_div(red, RAGGED_BK);
+    const int halves = ragged_halves(k->swap, k->pair, k->bn);
+    p.nkb = (int)ceil_div(red, 64 * halves);
     long tiles;
     if (tn) {
         p.x_blocks = (int)ceil_div(N, bm);
@@ -193,7 +194,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     p.idesc = ragged_idesc(bf16, x_mn, y_mn, bm, k->bn);
 
     // shared memory: the deepest operand ring beside the output staging
-    const uint32_t stage = 128u * 128u + y_rows * 128u;
+    const uint32_t stage = (uint32_t)halves * (128u * 128u + y_rows * 128u);
     const int slots = k->swap ? 0 : k->pair ? 1 : 2;
     int stages = RAGGED_MAX_STAGES;
     for (; stages >= 2; --stages) {

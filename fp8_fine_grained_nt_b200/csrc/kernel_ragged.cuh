@@ -52,9 +52,14 @@ struct RaggedTraits {
     static constexpr bool X_MN = TN || (DIR == RAGGED_NN && SWAP);
     static constexpr bool Y_MN = TN || (DIR == RAGGED_NN && !SWAP);
     static_assert(!Y_MN || Y_ROWS % 64 == 0, "MN-major operands load in 64-wide chunks");
-    static constexpr uint32_t X_BYTES = 128 * 128;
+    static constexpr uint32_t X_BYTES = 128 * 128; // 64 of the reduction
     static constexpr uint32_t Y_BYTES = Y_ROWS * 128;
-    static constexpr uint32_t STAGE_BYTES = X_BYTES + Y_BYTES;
+    static constexpr uint32_t HALF_BYTES = X_BYTES + Y_BYTES;
+    // 64-wide blocks of the reduction per stage: with two, one wait and one
+    // commit serve eight MMAs
+    static constexpr int H = ragged_halves(SWAP, PAIR, BN);
+    static constexpr int BK = 64 * H;
+    static constexpr uint32_t STAGE_BYTES = H * HALF_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "power of two, at most 512");
 };
@@ -79,7 +84,7 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv &f)
 // both operands in L2 (measured at 8192 x 8192 x 8192: bands of 8 741 us, of 4
 // 756 us, of 16 754 us).  SWAP: the token blocks of one weight block run side
 // by side.
-template <int DIR, bool SWAP, int BM, int BN>
+template <int DIR, bool SWAP, int BM, int BN, int BK>
 __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, int &g, const int *tiles,
                                                   const int *first, const int *count)
 {
@@ -129,7 +134,7 @@ __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, 
         r.i0 = (band * 8 + in_band - y * min(width, 8)) * BM;
         r.j0 = y * BN;
     }
-    r.nkb = TN ? (r.rows + RAGGED_BK - 1) / RAGGED_BK : p.nkb;
+    r.nkb = TN ? (r.rows + BK - 1) / BK : p.nkb;
     return r;
 }
 
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     using T = RaggedTraits<DIR, SWAP, PAIR, BN>;
     constexpr bool TN = T::TN;
     constexpr bool F32 = DIR == RAGGED_TN32;
+    constexpr int PARTIAL = RAGGED_PARTIAL / T::BK; // stages per partial sum
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             uint32_t plain = 0, uses = 0;
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
                 const int x_mn = ti.i0 + (PAIR ? (int)rank * 128 : 0) + ((!TN && !SWAP) ? ti.first : 0);
                 const int y_mn = ti.j0 + (PAIR ? (int)rank * T::Y_ROWS : 0) + (SWAP ? ti.first : 0);
                 const int red0 = TN ? ti.first : 0;
@@ -321,24 +327,31 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         break;
                     }
                     uint8_t *dst = smem + s * T::STAGE_BYTES;
-                    const int red = red0 + kb * RAGGED_BK;
-                    const bool tail = TN && ti.rows - kb * RAGGED_BK < RAGGED_BK;
+                    const int red = red0 + kb * T::BK;
+                    const bool tail = TN && ti.rows - kb * T::BK < T::BK;
                     if (tail) {
                         // counted by each CTA for itself: warp 2 clears the
                         // rows of other segments before the MMAs read them
                         mbar_arrive_expect_tx(&tail_full[s], T::STAGE_BYTES);
                         const uint32_t bar = smem_addr(&tail_full[s]);
-                        ragged_load<T::X_MN, false, false, 128>(dst, &tmap_x, bar, x_mn, red, ti.g);
-                        ragged_load<T::Y_MN, false, false, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn, red, ti.g);
+#pragma unroll
+                        for (int h = 0; h < T::H; ++h, dst += T::HALF_BYTES) {
+                            ragged_load<T::X_MN, false, false, 128>(dst, &tmap_x, bar, x_mn, red + 64 * h, ti.g);
+                            ragged_load<T::Y_MN, false, false, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn,
+                                                                          red + 64 * h, ti.g);
+                        }
                         plain &= ~(1u << s);
                     } else {
                         if (leader)
                             mbar_arrive_expect_tx(&full[s], PAIR ? 2 * T::STAGE_BYTES : T::STAGE_BYTES);
                         const uint32_t bar =
                             PAIR ? map_shared_rank(smem_addr(&full[s]), 0u) : smem_addr(&full[s]);
-                        ragged_load<T::X_MN, SWAP, PAIR, 128>(dst, &tmap_x, bar, x_mn, red, ti.g);
-                        ragged_load<T::Y_MN, !TN && !SWAP, PAIR, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn, red,
-                                                                           ti.g);
+#pragma unroll
+                        for (int h = 0; h < T::H; ++h, dst += T::HALF_BYTES) {
+                            ragged_load<T::X_MN, SWAP, PAIR, 128>(dst, &tmap_x, bar, x_mn, red + 64 * h, ti.g);
+                            ragged_load<T::Y_MN, !TN && !SWAP, PAIR, T::Y_ROWS>(dst + T::X_BYTES, &tmap_y, bar, y_mn,
+                                                                               red + 64 * h, ti.g);
+                        }
                         plain |= 1u << s;
                         uses ^= 1u << s;
                     }
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             uint32_t full_phase = 0, tail_phase = 0; // TN: per stage
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
                 if (ti.nkb == 0)
                     continue;
                 uint32_t buf = tile_it & 1;
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     break;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
                     // FP32 results: a fresh accumulator for each partial sum
-                    if (F32 && kb > 0 && kb % RAGGED_PARTIAL == 0) {
+                    if (F32 && kb > 0 && kb % PARTIAL == 0) {
                         buf = ++tile_it & 1;
                         if (!wait_ragged(&acc_empty[buf], ((tile_it >> 1) & 1) ^ 1, abort_flag, p)) {
                             ok = false;
@@ -388,11 +401,11 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         }
                     }
                     const uint32_t d = tmem_base + buf * (uint32_t)BN;
-                    const bool first_kb = F32 ? kb % RAGGED_PARTIAL == 0 : kb == 0;
-                    int steps = RAGGED_BK / 16;
+                    const bool first_kb = F32 ? kb % PARTIAL == 0 : kb == 0;
+                    int steps = T::BK / 16;
                     if constexpr (TN) {
                         // a segment's last block is announced by warp 2
-                        const bool tail = ti.rows - kb * RAGGED_BK < RAGGED_BK;
+                        const bool tail = ti.rows - kb * T::BK < T::BK;
                         if (!wait_ragged(tail ? &tail_ready[s] : &full[s],
                                          ((tail ? tail_phase : full_phase) >> s) & 1, abort_flag, p)) {
                             ok = false;
@@ -400,7 +413,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         }
                         if (tail) {
                             tail_phase ^= 1u << s;
-                            steps = (ti.rows - kb * RAGGED_BK + 15) / 16;
+                            steps = (ti.rows - kb * T::BK + 15) / 16;
                         } else {
                             full_phase ^= 1u << s;
                         }
@@ -412,15 +425,16 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     const uint64_t xd = x0 + s * (T::STAGE_BYTES >> 4);
                     const uint64_t yd = y0 + s * (T::STAGE_BYTES >> 4);
 #pragma unroll
-                    for (int k = 0; k < RAGGED_BK / 16; ++k)
+                    for (int k = 0; k < T::BK / 16; ++k)
                         if (!TN || k < steps)
-                            mma_f16<PAIR>(d, xd + k * X_STEP, yd + k * Y_STEP, p.idesc,
+                            mma_f16<PAIR>(d, xd + (k / 4) * (T::HALF_BYTES >> 4) + (k % 4) * X_STEP,
+                                          yd + (k / 4) * (T::HALF_BYTES >> 4) + (k % 4) * Y_STEP, p.idesc,
                                           (!first_kb || k > 0) ? 1u : 0u);
                     if constexpr (PAIR)
                         mma_commit_pair_mc(&empty[s], 0x3);
                     else
                         mma_commit(&empty[s]);
-                    if (kb == ti.nkb - 1 || (F32 && kb % RAGGED_PARTIAL == RAGGED_PARTIAL - 1)) {
+                    if (kb == ti.nkb - 1 || (F32 && kb % PARTIAL == PARTIAL - 1)) {
                         if constexpr (PAIR)
                             mma_commit_pair_mc(&acc_full[buf], 0x3);
                         else
@@ -452,11 +466,11 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             uint32_t s = 0, tail_phase = 0;
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
-                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
+                const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
                 s += (uint32_t)ti.nkb;
                 while (s >= stages)
                     s -= stages;
-                const int valid = ti.rows & (RAGGED_BK - 1);
+                const int valid = ti.rows & (T::BK - 1);
                 if (valid == 0)
                     continue;
                 const uint32_t st = s == 0 ? stages - 1 : s - 1; // the segment's last block
@@ -468,13 +482,13 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     break;
                 }
                 tail_phase ^= 1u << st;
-                constexpr int CHUNKS = (int)(T::STAGE_BYTES / 8192);
+                constexpr int CHUNKS = (int)(T::HALF_BYTES / 8192);
                 const int end = (valid + 15) & ~15; // the MMAs' steps of 16 end here
                 const uint32_t at = smem_addr(smem) + st * T::STAGE_BYTES + (lane & 7) * 16;
                 for (int r = valid + (lane >> 3); r < end; r += 4)
 #pragma unroll
                     for (int c = 0; c < CHUNKS; ++c)
-                        st_shared_v4(at + c * 8192 + r * 128, 0u, 0u, 0u, 0u);
+                        st_shared_v4(at + (r >> 6) * T::HALF_BYTES + c * 8192 + (r & 63) * 128, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         const bool bf16 = p.out_type == RAGGED_OUT_BF16;
         uint32_t tile_it = 0, slot = 0;
         for (int t = t_first; t < num_tiles; t += t_stride) {
-            const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN>(p, t, group, tiles, first, count);
+            const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
             const bool zero = ti.nkb == 0; // TN: a group without rows
             if (zero && p.accumulate)
                 continue;
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 for (int c = 0; c < NC; ++c)
                     acc[c] = 0.0f;
                 bool got = true;
-                for (int kb = 0; kb < ti.nkb; kb += RAGGED_PARTIAL, ++tile_it) {
+                for (int kb = 0; kb < ti.nkb; kb += PARTIAL, ++tile_it) {
                     const uint32_t buf = tile_it & 1;
                     got = wait_ragged(&acc_full[buf], (tile_it >> 1) & 1, abort_flag, p);
                     got = __all_sync(0xffffffffu, got);

@@ -11,9 +11,13 @@ namespace fp8nt {
 enum RaggedDir : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2, RAGGED_TN32 = 3 }; // TN32: FP32 result
 enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 = 2 };
 
-constexpr int RAGGED_BK = 64;           // reduction elements per stage: 128-byte swizzled rows
+// 64-wide blocks of the reduction (128-byte swizzled rows) per stage
+__host__ __device__ constexpr int ragged_halves(bool swap, bool pair, int bn)
+{
+    return pair ? 2 : swap ? 1 : 1;
+}
 constexpr int RAGGED_THREADS = 384;     // 12 warps, 8 of them in the epilogue
-constexpr int RAGGED_PARTIAL = 8;       // TN32: blocks of the reduction per partial sum
+constexpr int RAGGED_PARTIAL = 512;     // TN32: rows per partial sum
 constexpr int RAGGED_REGS_OTHER = 56;   // TN32: registers of warps 0-3 and of the epilogue warps
 constexpr int RAGGED_REGS_EPILOGUE = 224;
 static_assert(4 * 32 * RAGGED_REGS_OTHER + 8 * 32 * RAGGED_REGS_EPILOGUE <= RAGGED_THREADS * REGS_AT_LAUNCH,
