@@ -41,23 +41,23 @@ constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, wit
 // 1.7 GHz), so the products that a form issues for padding rows cost time even
 // where memory bounds the call.  The constants were fitted to calls measured
 // that way on B200 (2 to 256 rows per group in 8 to 64 groups for NT and NN,
-// every form; the form taken is 1 % slower than the best on average, 20 % at
+// every form; the form taken is 1 % slower than the best on average, 10 % at
 // most) and, for TN, to 18 calls of 16 to 1024 rows per group (1 %, 8 %).
 // Some of them, us (SWAP by BN):
 //                                           16   32   64  128  128x256  pair
-//   NT 16 groups, N=4096, K=7168,  8 rows  157  166  174  187      169   213
-//                                 64 rows  621  333  253  211      186   252
-//                                256 rows             626  464     361   362
-//   NN  8 groups, N=7168, K=2048, 16 rows   78   42   45   48       61    57
-//                                128 rows       151  116   87       73    70
-//   NN 64 groups, N=2112, K=2048, 16 rows  128   96  103  116      107   142
+//   NT 16 groups, N=4096, K=7168,  8 rows  146  152  158  170      161   209
+//                                 64 rows  442  258  213  192      179   237
+//                                256 rows             499  388      331   347
+//   NN  8 groups, N=7168, K=2048, 16 rows   58   36   38   44       51    55
+//                                128 rows       109   90   78       65    67
+//   NN 64 groups, N=2112, K=2048, 16 rows  104   87   92  108      102   137
 //                                          128x128  128x256  pair
 //   TN 64 groups, N=2048, K=520, 64 rows        43       46    48
 //                              1024 rows       259      229   190
 //   TN  8 groups, N=7168, K=2048, 16 rows       53       46    49
 double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K, int sms)
 {
-    const double cycles_per_us = 1900.0, bytes_per_us = 6.7e6;
+    const double cycles_per_us = 1900.0;
     const double used = groups < rows ? groups : rows, mean = (double)rows / used;
     const double units = k.pair ? (sms > 1 ? sms / 2 : 1) : sms;
     const int bm = k.pair ? 256 : 128;
@@ -69,7 +69,7 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
         const double blocks = ceil(mean / 64.0) * (mma > load ? mma : load) + 1100.0;
         const double epilogue = 700.0 + 1450.0 * k.bn / 128.0;
         const double busy = ceil(tiles / units) * (blocks > epilogue ? blocks : epilogue) / cycles_per_us;
-        const double memory = ((k.dir == RAGGED_TN32 ? 4.0 : 2.0) * groups * N * K + 2.0 * rows * ((double)N + K)) / bytes_per_us;
+        const double memory = ((k.dir == RAGGED_TN32 ? 4.0 : 2.0) * groups * N * K + 2.0 * rows * ((double)N + K)) / 7.0e6;
         return busy > memory ? busy : memory;
     }
     const double out = k.dir == RAGGED_NT ? N : K, red = k.dir == RAGGED_NT ? K : N;
@@ -77,10 +77,10 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
     const double tok = 2 * mean <= block ? 1.0 : mean / block + 0.5; // token blocks of a group
     const double tiles = ceil(used * tok * ceil(out / wide));
     const double blocks = ceil(red / 64.0);
-    const double mma = (k.swap ? 2.0 * (k.bn < 32 ? 32 : k.bn) : 512.0) + 425.0, load = stage / 44.0;
-    const double tile = (blocks * (mma > load ? mma : load) + 4790.0) / cycles_per_us;
-    const double weights = 2.0 * wide * red / tok / bytes_per_us; // read from memory for one tile
-    const double power = 2.0 * tiles * bm * k.bn * blocks * 64.0 / 1.96e10; // all products, padding too
+    const double mma = (k.swap ? 2.0 * (k.bn < 32 ? 32 : k.bn) : 512.0) + 152.0, load = stage / 61.0;
+    const double tile = (blocks * (mma > load ? mma : load) + 4670.0) / cycles_per_us;
+    const double weights = 2.0 * wide * red / tok / 8.5e6; // read from memory for one tile
+    const double power = 2.0 * tiles * bm * k.bn * blocks * 64.0 / 4.0e9; // all products, padding too
     const double full = floor(tiles / units), rest = tiles - full * units;
     const double wave = tile > units * weights ? tile : units * weights;
     const double last = rest <= 0 ? 0 : tile > rest * weights ? tile : rest * weights;
@@ -195,7 +195,9 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
 
     // shared memory: the deepest operand ring beside the output staging
     const uint32_t stage = (uint32_t)halves * (128u * 128u + y_rows * 128u);
-    const int slots = k->swap ? 0 : k->pair ? 1 : 2;
+    // (one slot per epilogue warp beside the wide tiles: the stage it leaves room
+    // for is worth more, 149 -> 142 us for 128 rows over 16 groups)
+    const int slots = k->swap ? 0 : k->bn == 256 ? 1 : 2;
     int stages = RAGGED_MAX_STAGES;
     for (; stages >= 2; --stages) {
         make_ragged_plan(p, stage, stages, slots);
