@@ -480,6 +480,7 @@ def group_rows_by_index(index: torch.Tensor, num_groups: int, offsets: torch.Ten
             return offsets, order, slots, m_indices
         if status > 0:
             raise Fp8NtError(status, "group_rows_by_index")
+    num_groups, alignment = int(num_groups), int(alignment)
     device = _device_of(index, "index")
     if index.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"index has dtype {index.dtype}, expected int32 or int64")

@@ -1091,7 +1091,7 @@ const char *dg_status_string(int status)
     case DG_ERR_UNSUPPORTED_ARCH: return "current device is not sm_100 (B200)";
     case DG_ERR_CUDA: return "CUDA call failed";
     case DG_ERR_DEVICE_TIMEOUT: return "device pipeline wait timed out";
-    case DG_ERR_DEVICE_BAD_INDEX: return "masked_m or m_indices out of range";
+    case DG_ERR_DEVICE_BAD_INDEX: return "masked_m, m_indices or another index out of range";
     default: return "unknown status";
     }
 }

@@ -122,8 +122,9 @@ int check_ragged(int dir, const void *A, const void *B, void *D, const int *offs
     // bytes of one group's weights: the stride of a tensor map's group axis
     if ((uint64_t)N * (uint64_t)K * 4u >= (1ull << 40))
         return DG_ERR_UNSUPPORTED_SHAPE;
-    // tiles of the smallest tile form are counted in 32 bits
-    if ((ceil_div(M_sum, 32) + G) * ceil_div(N > K ? N : K, 128) > 0x7fffffffL ||
+    // rows are 32-bit coordinates, with room for the last tile, and the tiles of
+    // the smallest tile form are counted in 32 bits
+    if (M_sum > 0x7fff0000 || (ceil_div(M_sum, 16) + G) * ceil_div(N > K ? N : K, 128) > 0x7fffffffL ||
         (long)G * ceil_div(N, 128) * ceil_div(K, 128) > 0x7fffffffL)
         return DG_ERR_UNSUPPORTED_SHAPE;
     // without rows only the weight gradient has anything to write

@@ -59,7 +59,7 @@ typedef enum dg_status {
     DG_ERR_UNSUPPORTED_ARCH = 4,  /* current device is not sm_100 */
     DG_ERR_CUDA = 5,              /* a CUDA runtime/driver call failed */
     DG_ERR_DEVICE_TIMEOUT = 6,    /* device: a pipeline wait ran out (kernel exited early) */
-    DG_ERR_DEVICE_BAD_INDEX = 7   /* device: masked_m / m_indices out of range */
+    DG_ERR_DEVICE_BAD_INDEX = 7   /* device: masked_m, m_indices, offsets, order or index out of range */
 } dg_status;
 
 /* Dense GEMM (DeepGEMM README, usage: deep_gemm.gemm_fp8_fp8_bf16_nt, the
@@ -150,7 +150,7 @@ int quantize_fp8_1x128(const void *x, int x_dtype, void *q, float *sa, int M, in
  *            sets DG_ERR_DEVICE_BAD_INDEX and is clamped to [0, M_sum] and to
  *            the segment's start.
  * Everything row-major and dense; N % 8 == 0, K % 8 == 0 (16-byte rows),
- * 1 <= num_groups <= 1024, M_sum >= 0.  Sums are FP32 over the whole
+ * 1 <= num_groups <= 1024, 0 <= M_sum <= 0x7fff0000.  Sums are FP32 over the whole
  * reduction, rounded once (to nearest even) to D's type.  D must not overlap
  * A or B. */
 

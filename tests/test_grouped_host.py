@@ -31,7 +31,8 @@ def test_ragged_rows_refusals(lib, name):
     assert f(P, P, P, P, BF16, 2, 64, 64, 4, None) == 3        # K % 8
     assert f(P, P, P, P, BF16, 2, 64, 0, 64, None) == 3
     assert f(P, P, P, P, BF16, 1024, 64, 1 << 20, 1 << 20, None) == 3   # a group's weights over 2^40 bytes
-    assert f(P, P, P, P, BF16, 1024, 2 ** 31 - 8, 1 << 18, 64, None) == 3  # tiles over 2^31
+    assert f(P, P, P, P, BF16, 1024, 2 ** 30, 1 << 18, 64, None) == 3      # tiles over 2^31
+    assert f(P, P, P, P, BF16, 4, 2 ** 31 - 1, 64, 64, None) == 3          # rows
     for bad in range(4):
         args = [P] * 4
         args[bad] = NULL

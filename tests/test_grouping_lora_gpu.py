@@ -216,6 +216,25 @@ def test_lora_special_values_stay_in_their_rows():
     assert torch.equal(bad, want)
 
 
+def test_lora_special_values_in_long_batches():
+    """The same where 128 slots of up to three adapters are computed together."""
+    T, L, R, N, K = 300, 3, 16, 136, 264
+    x, c = gen(T, K, seed=1, dtype=BF16), gen(T, N, seed=2, dtype=BF16)
+    A, B = gen(L, R, K, seed=3, dtype=BF16, scale=K ** -0.5), gen(L, N, R, seed=4, dtype=BF16)
+    x[3, 5] = float("nan")
+    A[1, 2, 7] = float("inf")
+    B[2, 11, 0] = float("inf")
+    ids = [0] * 100 + [1] * 60 + [2] * 140
+    d = torch.zeros(T, N, dtype=BF16, device="cuda")
+    fp8.m_grouped_lora_add(x, A, B, torch.ones(L, device="cuda"), c, d, torch.tensor(ids, dtype=torch.int32).cuda())
+    bad = ~torch.isfinite(d)
+    want = torch.zeros_like(bad)
+    want[3] = True
+    want[100:160] = True
+    want[160:, 11] = True
+    assert torch.equal(bad, want)
+
+
 def test_lora_fp16_middle_result_beyond_its_range():
     """x . A^T is about 2e6, beyond FP16; B brings the result back into it."""
     T, L, R, N, K = 20, 1, 16, 136, 512
@@ -278,6 +297,64 @@ def test_lora_graph_and_concurrent_streams():
     torch.cuda.synchronize()
     for d in outs + eager:
         assert torch.equal(d, want)
+
+
+def test_lora_rows_beyond_2_to_31_elements():
+    T, L, R, N, K = 70001, 2, 8, 32768, 64
+    x, A = gen(T, K, seed=1, dtype=BF16), gen(L, R, K, seed=2, dtype=BF16, scale=K ** -0.5)
+    B, d = gen(L, N, R, seed=3, dtype=BF16), torch.zeros(T, N, dtype=BF16, device="cuda")
+    ids = (torch.arange(T, device="cuda") >= 35000).to(torch.int32)
+    zero = torch.zeros(40, N, dtype=BF16, device="cuda")
+    for slots in (T, 40):   # a long batch, and a few rows at the end
+        d.zero_()
+        order = torch.arange(T - slots, T, dtype=torch.int32, device="cuda")
+        fp8.m_grouped_lora_add(x, A, B, torch.ones(L, device="cuda"), d, d, ids[T - slots:], order)
+        lora_check(d[T - 40:], x[T - 40:], A[1], B[1], 1.0, zero)
+        if slots == T:
+            lora_check(d[34960:35000], x[34960:35000], A[0], B[0], 1.0, zero)
+
+
+def test_lora_many_adapters_and_long_batches():
+    """The forms for few and for many slots on the same rows agree to rounding."""
+    T, R, N, K = 1000, 16, 264, 520
+    ids = [t * 7 // T for t in range(T)]
+    lora_case(T, 7, R, N, K, FP16, ids, seed=3)              # about 143 rows each: the long form
+    lora_case(T, 200, R, N, K, FP16, ids, seed=3)            # 200 adapters loaded, 7 in use: the short one
+    lora_case(T, 31, 64, N, K, BF16, [t % 31 for t in range(T)], seed=4)   # unsorted: 128 segments a block
+
+
+def test_refusals_of_device_tensors():
+    x, A, B, c = (gen(4, 64, seed=1, dtype=BF16), gen(2, 8, 64, seed=2, dtype=BF16), gen(2, 64, 8, seed=3, dtype=BF16),
+                  gen(4, 64, seed=4, dtype=BF16))
+    s, m = torch.ones(2, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in ((x.float(), A, B, s, c, c, m), (x, A.half(), B, s, c, c, m), (x, A, B, s.double(), c, c, m),
+                (x, A, B, s, c.half(), c, m), (x, A, B, s, c, c, m.long())):
+        with pytest.raises(TypeError):
+            fp8.m_grouped_lora_add(*bad)
+    for bad in ((x, A.transpose(1, 2), B, s, c, c, m), (x, A, B, s, c.t().contiguous().t(), c, m),
+                (x, A, B, s, c[:3], c, m), (x, A, B, s, c, c, torch.zeros(5, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            fp8.m_grouped_lora_add(*bad)
+    with pytest.raises(ValueError):
+        fp8.m_grouped_lora_add(x, A, B, s, c, c, m, workspace=torch.empty(64, dtype=torch.uint8))
+    with pytest.raises(fp8.Fp8NtError) as e:
+        fp8.m_grouped_lora_add(x, A, B, s, c, c, m, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 1
+    wide = gen(4, 68, seed=5, dtype=BF16)
+    with pytest.raises(fp8.Fp8NtError) as e:   # rows 136 bytes apart
+        fp8.m_grouped_lora_add(wide[:, :64], A, B, s, c, c, m)
+    assert e.value.status == 3
+    i32 = dict(dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        fp8.group_rows_by_index(s, 4, torch.empty(5, **i32), torch.empty(2, **i32))
+    with pytest.raises(ValueError):
+        fp8.group_rows_by_index(m, 4, torch.empty(5, **i32), torch.empty(3, **i32))
+    with pytest.raises(fp8.Fp8NtError):
+        fp8.group_rows_by_index(m, 0, torch.empty(1, **i32), torch.empty(4, **i32))
+    with pytest.raises(fp8.Fp8NtError):
+        fp8.group_rows_by_index(torch.zeros(9000, **i32), 4, torch.empty(5, **i32), torch.empty(9000, **i32),
+                                workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    assert fp8.get_device_status() == 0
 
 
 # ------------------------------------------------------------------ together

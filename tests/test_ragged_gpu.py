@@ -310,10 +310,58 @@ def test_repeated_calls_are_bit_equal():
         assert torch.equal(d, first)
 
 
-def test_sm_bound():
+@pytest.mark.parametrize("sms", [1, 2, 3])
+def test_sm_bound(sms):
     try:
-        fp8.set_num_sms(3)
+        fp8.set_num_sms(sms)
         run_rows("nt", [30, 400, 0, 200], 520, 136, BF16)
         run_tn([30, 400, 0, 200], 520, 264, BF16, FP32)
     finally:
         fp8.set_num_sms(0)
+
+
+def test_results_beyond_2_to_31_elements():
+    """Rows and groups whose offset in the result does not fit 32 bits."""
+    T, N, K = 70001, 32768, 8
+    a, b = gen(T, K, seed=1, dtype=BF16), gen(2, N, K, seed=2, dtype=BF16)
+    offsets = torch.tensor([0, 35000, T - 1], dtype=torch.int32, device="cuda")
+    d = torch.zeros(T, N, dtype=BF16, device="cuda")
+    fp8.m_grouped_gemm_nt_ragged(a, b, d, offsets)
+    for rows, g in ((slice(0, 40), 0), (slice(34990, 35000), 0), (slice(35000, 35010), 1), (slice(T - 30, T - 1), 1)):
+        w = b[g].double().T
+        check(d[rows], a[rows].double() @ w, a[rows].double().abs() @ w.abs(), K)
+    assert (d[T - 1] == 0).all()
+    del d
+    G, N, K = 40, 8192, 8192
+    offsets = torch.arange(G + 1, dtype=torch.int32, device="cuda") * 3
+    a, b = gen(3 * G, N, seed=3, dtype=BF16), gen(3 * G, K, seed=4, dtype=BF16)
+    d = torch.empty(G, N, K, dtype=BF16, device="cuda")
+    fp8.k_grouped_gemm_tn_ragged(a, b, d, offsets)
+    for g in (0, 31, 32, G - 1):
+        x, y = a[3 * g:3 * g + 3].double(), b[3 * g:3 * g + 3].double()
+        check(d[g, -64:], (x.T @ y)[-64:], (x.abs().T @ y.abs())[-64:], 3)
+
+
+def test_refusals_of_device_tensors():
+    a, b, d = gen(8, 64, seed=1, dtype=BF16), gen(2, 64, 64, seed=2, dtype=BF16), gen(8, 64, seed=3, dtype=BF16)
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    for bad in ((a.float(), b, d, off), (a, b.half(), d, off), (a, b, d.float(), off), (a, b, d, off.long())):
+        with pytest.raises(TypeError):
+            fp8.m_grouped_gemm_nt_ragged(*bad)
+    for bad in ((a.t().contiguous().t(), b, d, off), (a, b.transpose(1, 2), d, off), (a, b, d, off.cpu()),
+                (a, b, d, off[:2]), (a[:4], b, d, off), (a, b[0], d, off)):
+        with pytest.raises(ValueError):
+            fp8.m_grouped_gemm_nt_ragged(*bad)
+    wide = gen(8 * 64 + 4, seed=4, dtype=BF16)
+    with pytest.raises(fp8.Fp8NtError) as e:   # 8 bytes off a 16-byte boundary
+        fp8.m_grouped_gemm_nt_ragged(wide[4:].view(8, 64), b, d, off)
+    assert e.value.status == 2
+    with pytest.raises(fp8.Fp8NtError) as e:
+        fp8.m_grouped_gemm_nt_ragged(a[:, :4].contiguous(), b[:, :, :4].contiguous(), d, off)
+    assert e.value.status == 3
+    w = gen(2, 64, 64, seed=5, dtype=BF16)
+    with pytest.raises(TypeError):
+        fp8.k_grouped_gemm_tn_ragged(a, d, w, off, accumulate=True)
+    with pytest.raises(TypeError):
+        fp8.k_grouped_gemm_tn_ragged(a, d, w.half(), off)
+    assert fp8.get_device_status() == 0
