@@ -68,7 +68,7 @@ struct WidePlan {
 struct WideParams {
     LoraParams p;
     WidePlan plan;
-    uint32_t idesc1, idesc2;
+    uint32_t idesc; // of the MMAs, without the number of columns
     uint64_t timeout_ns;
 };
 
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     // cluster as a whole reads and writes long runs of each row (kbs below)
     const int n_tiles = ((p.N + 127) / 128 - rank + cl - 1) / cl;
     const int chunks = (p.R + 63) / 64;
+    const int ranks = (p.R + 15) / 16 * 16; // columns of an adapter in phase 1
     const int pitch = p.R + 4; // floats per row of the exchanged shares
 
     // ring positions, kept over the passes by each role
@@ -207,12 +208,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
     for (int seg0 = 0; seg0 < total_segs; seg0 += plan.segs, ++pass_it) {
         const int segs = min(plan.segs, total_segs - seg0);
-        // 128 of k per stage (two 64-wide swizzled halves: fewer waits) where
-        // three such stages fit, else 64
-        const uint32_t half_bytes = WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes;
-        const int halves = 6 * half_bytes <= plan.ring ? 2 : 1, bk = 64 * halves;
-        const uint32_t stage_bytes = halves * half_bytes;
-        const int kbs = ((p.K + bk - 1) / bk - rank + cl - 1) / cl;
+        const uint32_t stage_bytes = WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes; // 64 of k
+        const int kbs = ((p.K + 63) / 64 - rank + cl - 1) / cl;
         const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 3
         // a walk along the first ring: stage, and which of its uses in this pass is odd
         struct Ring {
@@ -246,7 +243,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
         // ------------------------------------------------------------ phase 1
         if (warp < 4) {
-            // thread: 16-byte piece lane % 8 of both halves of rows 32 warp + 4 j + lane / 8
+            // thread: 16-byte piece lane % 8 of rows 32 warp + 4 j + lane / 8
             const int piece = lane & 7;
             const uint16_t *src[8];
             uint32_t live = 0;
@@ -261,7 +258,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const uint32_t dst = (uint32_t)((warp * 32 + (lane >> 3)) * 128);
             // a stage is published once its copies have landed, `lag` rounds
             // after they were issued
-            constexpr int lag = 2; // less than the stages there are
+            const int lag = s1 >= 6 ? 4 : 2; // less than the stages there are
             Ring at = {0, s1, 0u}, behind = {0, s1, 0u};
             auto publish = [&]() {
                 fence_proxy_async_smem();
@@ -276,20 +273,21 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (!ok)
                     break;
                 const uint32_t to = base + at.s * stage_bytes + dst;
-                for (int h = 0; h < halves; ++h) {
-                    const int k = (i * cl + rank) * bk + h * 64;
-                    const bool k_in = k + piece * 8 < p.K;
+                const int k = (i * cl + rank) * 64;
+                const bool k_in = k + piece * 8 < p.K;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int r = 4 * j + (lane >> 3); // (its low 3 bits are the row's)
-                        const bool in = k_in && ((live >> j) & 1u);
-                        cp_async_16(to + h * WIDE_X_BYTES + j * 512 + ((piece ^ (r & 7)) << 4),
-                                    in ? src[j] + k : static_cast<const uint16_t *>(p.x), in);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + (lane >> 3); // (its low 3 bits are the row's)
+                    const bool in = k_in && ((live >> j) & 1u);
+                    cp_async_16(to + j * 512 + ((piece ^ (r & 7)) << 4),
+                                in ? src[j] + k : static_cast<const uint16_t *>(p.x), in);
                 }
                 cp_async_commit();
                 if (i >= lag) {
-                    cp_async_wait<lag>();
+                    if (lag == 4)
+                        cp_async_wait<4>();
+                    else
+                        cp_async_wait<2>();
                     publish();
                 }
             }
@@ -303,12 +301,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     const int s = at.s;
                     if (!(ok = wait(&empty1[s], parity1(at) ^ 1u)))
                         break;
-                    mbar_arrive_expect_tx(&full1[s], (uint32_t)(halves * segs) * plan.a_bytes);
-                    uint8_t *dst = smem + s * stage_bytes + halves * WIDE_X_BYTES;
-                    for (int h = 0; h < halves; ++h) // (a half past K is zeros)
-                        for (int j = 0; j < segs; ++j, dst += plan.a_bytes)
-                            tma_load_nd<true, false>(dst, &tmap_a, smem_addr(&full1[s]),
-                                                     (i * cl + rank) * bk + h * 64, 0, seg_adapter[seg0 + j]);
+                    mbar_arrive_expect_tx(&full1[s], (uint32_t)segs * plan.a_bytes);
+                    for (int j = 0; j < segs; ++j)
+                        tma_load_nd<true, false>(smem + s * stage_bytes + WIDE_X_BYTES + j * plan.a_bytes, &tmap_a,
+                                                 smem_addr(&full1[s]), (i * cl + rank) * 64, 0,
+                                                 seg_adapter[seg0 + j]);
                 }
                 // the first stages of B, while the products of phase 1 run
                 for (; b_done < min(b_loads, (int)s2); ++b_done)
@@ -316,24 +313,18 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
         } else if (warp == 4) {
             if (lane == 0) {
+                const uint32_t idesc1 = wp.idesc | (uint32_t)(segs * ranks >> 3) << 17;
                 Ring at = {0, s1, 0u};
                 for (int i = 0; ok && i < kbs; ++i, at.skip(1)) {
                     const int s = at.s;
                     if (!(ok = wait(&full1[s], parity1(at))))
                         break;
                     tc_fence_after();
-                    const uint32_t at_x = base + s * stage_bytes;
-                    uint32_t at_a = at_x + halves * WIDE_X_BYTES;
-                    for (int h = 0; h < halves; ++h) {
-                        const uint64_t xd = make_sdesc(at_x + h * WIDE_X_BYTES);
-                        for (int j = 0; j < segs; ++j, at_a += plan.a_bytes) {
-                            const uint64_t ad = make_sdesc(at_a);
+                    const uint64_t xd = make_sdesc(base + s * stage_bytes);
+                    const uint64_t ad = make_sdesc(base + s * stage_bytes + WIDE_X_BYTES);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16<false>(tmem + j * 128, xd + 2 * k, ad + 2 * k, wp.idesc1,
-                                               (i > 0 || h > 0 || k > 0) ? 1u : 0u);
-                        }
-                    }
+                    for (int k = 0; k < 4; ++k) // all adapters of the pass side by side
+                        mma_f16<false>(tmem, xd + 2 * k, ad + 2 * k, idesc1, (i > 0 || k > 0) ? 1u : 0u);
                     mma_commit(&empty1[s]);
                 }
                 mma_commit(p1_done);
@@ -357,7 +348,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     for (uint32_t left = present; left; left &= left - 1) {
                         const int i = __ffs(left) - 1;
                         float w[16];
-                        tmem_ld16(taddr + i * 128 + c, w);
+                        tmem_ld16(taddr + i * ranks + c, w);
                         tmem_wait_ld(w);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -479,11 +470,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     const int buf = acc_buf(t);
                     if (!(ok = wait(&acc_empty[buf], acc_parity(t) ^ 1u)))
                         break;
-                    for (int i = 0; ok && i < segs; ++i) {
+                    for (int i = 0; ok && i < segs;) {
                         const uint32_t d = tmem + (buf * segs + i) * 128;
-                        for (int rc = 0; rc < chunks; ++rc, ++it2) {
+                        // two adapters at once where their B lies side by side
+                        const int both = it2 % s2 == 0 && chunks == 1 && i + 1 < segs ? 2 : 1;
+                        const uint32_t idesc2 = wp.idesc | (uint32_t)(both * 128 >> 3) << 17;
+                        for (int rc = 0; ok && rc < chunks; ++rc, it2 += both) {
                             const uint32_t s = it2 % s2;
-                            if (!(ok = wait(&full2[s], (it2 / s2) & 1)))
+                            ok = wait(&full2[s], (it2 / s2) & 1);
+                            if (both == 2)
+                                ok = ok && wait(&full2[s + 1], (it2 / s2) & 1);
+                            if (!ok)
                                 break;
                             tc_fence_after();
                             const uint64_t bd = make_sdesc(base + plan.off_b + s * WIDE_B_BYTES);
@@ -493,11 +490,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                                 const uint64_t vd =
                                     make_sdesc(base + plan.off_v + (uint32_t)(term * chunks + rc) * WIDE_X_BYTES);
                                 for (int k = 0; k < steps; ++k)
-                                    mma_f16<false>(d, vd + 2 * k, bd + 2 * k, wp.idesc2,
+                                    mma_f16<false>(d, vd + 2 * k, bd + 2 * k, idesc2,
                                                    (rc > 0 || term > 0 || k > 0) ? 1u : 0u);
                             }
                             mma_commit(&empty2[s]);
+                            if (both == 2)
+                                mma_commit(&empty2[s + 1]);
                         }
+                        i += both;
                     }
                     mma_commit(&acc_full[buf]);
                 }
@@ -614,8 +614,8 @@ WidePlan wide_plan(int slots, int R)
     const uint32_t chunks = (uint32_t)(R + 63) / 64;
     w.segs = R <= 64 ? 4 : 1;
     w.a_bytes = (uint32_t)(R + 15) / 16 * 16 * 128;
-    // at least three stages of 64 of k (four adapters, or one above rank 64),
-    // three of 128 with one adapter up to rank 64; the shares (at most 68 KB) and two c buffers (64
+    // six stages of 64 of k with one adapter up to rank 64, at least three with
+    // four, or with one above; the shares (at most 68 KB) and two c buffers (64
     // KB, beside the shares up to rank 64) in the same room
     w.ring = R <= 64 ? 3u * 49152u : 98304u;
     w.off_c = R <= 64 ? align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024) : 0;
@@ -675,8 +675,7 @@ int launch_lora_wide(const LoraParams &p, bool bf16, const DeviceView &dev, cuda
     if ((int)wp.plan.total + 1024 > dev.max_smem - 4096)
         return DG_ERR_UNSUPPORTED_SHAPE;
     const int ranks = (p.R + 15) / 16 * 16;
-    wp.idesc1 = ragged_idesc(bf16, false, false, 128, ranks);
-    wp.idesc2 = ragged_idesc(bf16, false, false, 128, 128);
+    wp.idesc = ragged_idesc(bf16, false, false, 128, 0);
     wp.timeout_ns = dev.timeout_ns;
     const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap ta, tb;
