@@ -128,7 +128,7 @@ def load_library():
                                            Z, P]
         lib.get_lora_workspace_size.argtypes = [I, I, I, I, I]
         lib.get_lora_workspace_size.restype = L
-        lib.dg_force_ragged.argtypes = [I, I, I]
+        lib.dg_force_ragged.argtypes = [I, I, I, I]
         _lib = lib
         return lib
 
@@ -619,8 +619,10 @@ def force_tail_split(mode: int = 0) -> None:
     _check(load_library().dg_force_tail_split(int(mode)), "dg_force_tail_split")
 
 
-def force_ragged(swap_ab: int = 0, cta_pair: int = 0, block_n: int = 0) -> None:
-    """Pin the tile form of later ragged grouped calls (0, 0, 0 = automatic):
-    swap_ab 1 = weights on the 128-row side and block_n token rows; cta_pair 1 =
-    256 x 256 by CTA pairs; block_n alone = 128 x block_n.  For tests."""
-    _check(load_library().dg_force_ragged(int(swap_ab), int(cta_pair), int(block_n)), "dg_force_ragged")
+def force_ragged(swap_ab: int = 0, cta_pair: int = 0, block_n: int = 0, split: int = 0) -> None:
+    """Pin the tile form of later ragged grouped calls (0, 0, 0, 0 = automatic):
+    swap_ab 1 = weights on the 128-row side and block_n token rows, the reduction
+    shared by split CTAs; cta_pair 1 = 256 x 256 by CTA pairs; block_n alone = 128 x
+    block_n.  For tests."""
+    _check(load_library().dg_force_ragged(int(swap_ab), int(cta_pair), int(block_n), int(split)),
+           "dg_force_ragged")

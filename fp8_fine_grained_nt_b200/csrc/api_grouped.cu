@@ -27,13 +27,22 @@ const RaggedKernel kRagged[] = {
 };
 constexpr int kNumRagged = sizeof(kRagged) / sizeof(kRagged[0]);
 
-// test hook: swap (0 / 1), pair (0 / 1) and bn of later calls, 0 = automatic
+// test hook: bn, swap << 16, pair << 17 and split << 20 of later calls, 0 = automatic
 std::atomic<uint32_t> g_forced_ragged{0};
 
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, with room to round up
+
+// Clusters of `together` CTAs, one CTA per SM, that run at once on `sms` SMs:
+// clusters of 4 and 8 do not fill the GPCs of a 148-SM part (measured: 33, 15).
+int clusters_held(int together, int sms)
+{
+    const int most = together == 4 ? 33 : together == 8 ? 15 : 148 / together;
+    const int n = sms / together < most ? sms / together : most;
+    return n > 0 ? n : 1;
+}
 
 // Time of a call in us by a wave model of the tile forms, with the mean rows per
 // group (the host does not know more) and counts spread evenly from none to
@@ -55,11 +64,12 @@ constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, wit
 //   TN 64 groups, N=2048, K=520, 64 rows        43       46    48
 //                              1024 rows       259      229   190
 //   TN  8 groups, N=7168, K=2048, 16 rows       53       46    49
-double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K, int sms)
+double ragged_estimate(const RaggedKernel &k, int split, int groups, int rows, int N, int K, int sms)
 {
     const double cycles_per_us = 1900.0;
     const double used = groups < rows ? groups : rows, mean = (double)rows / used;
-    const double units = k.pair ? (sms > 1 ? sms / 2 : 1) : sms;
+    const int together = k.pair ? 2 : split;
+    const double units = clusters_held(together, sms);
     const int bm = k.pair ? 256 : 128;
     const double stage = 16384.0 + 128.0 * (k.pair ? k.bn / 2 : k.bn);
     if (k.dir == RAGGED_TN || k.dir == RAGGED_TN32) {
@@ -78,7 +88,9 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
     const double tiles = ceil(used * tok * ceil(out / wide));
     const double blocks = ceil(red / 64.0);
     const double mma = (k.swap ? 2.0 * (k.bn < 32 ? 32 : k.bn) : 512.0) + 152.0, load = stage / 61.0;
-    const double tile = (blocks * (mma > load ? mma : load) + 4670.0) / cycles_per_us;
+    // (sharing a tile takes an exchange of about 3000 cycles)
+    const double tile =
+        (ceil(blocks / split) * (mma > load ? mma : load) + 4670.0 + (split > 1 ? 3000.0 : 0.0)) / cycles_per_us;
     const double weights = 2.0 * wide * red / tok / 8.5e6; // read from memory for one tile
     const double power = 2.0 * tiles * bm * k.bn * blocks * 64.0 / 4.0e9; // all products, padding too
     const double full = floor(tiles / units), rest = tiles - full * units;
@@ -87,29 +99,39 @@ double ragged_estimate(const RaggedKernel &k, int groups, int rows, int N, int K
     return full * wave + last + power;
 }
 
-// The kernel of a call.
-const RaggedKernel *choose_ragged(int dir, int groups, int rows, int N, int K, int sms)
+// The kernel of a call, and the CTAs that share a tile's reduction.
+const RaggedKernel *choose_ragged(int dir, int groups, int rows, int N, int K, int sms, int *split)
 {
     const uint32_t forced = g_forced_ragged.load(std::memory_order_relaxed);
-    if (forced) {
-        for (int i = 0; i < kNumRagged; ++i) {
-            const RaggedKernel &k = kRagged[i];
-            if (k.dir == dir && ((uint32_t)k.bn | (uint32_t)k.swap << 16 | (uint32_t)k.pair << 17) == forced)
-                return &k;
-        }
-    }
-    const RaggedKernel *best = nullptr;
+    const int forced_split = (int)(forced >> 20);
+    const long blocks = ceil_div(dir == RAGGED_NT ? K : N, 128); // stages of the swapped tiles
+    const RaggedKernel *best = nullptr, *pinned = nullptr;
     double best_us = 0;
+    *split = 1;
     for (int i = 0; i < kNumRagged; ++i) {
-        if (kRagged[i].dir != dir)
+        const RaggedKernel &k = kRagged[i];
+        if (k.dir != dir)
             continue;
-        const double us = ragged_estimate(kRagged[i], groups, rows, N, K, sms);
-        if (!best || us < best_us) {
-            best = &kRagged[i];
-            best_us = us;
+        const bool is_pinned =
+            ((uint32_t)k.bn | (uint32_t)k.swap << 16 | (uint32_t)k.pair << 17) == (forced & 0xFFFFFu);
+        const int most = k.swap && k.bn <= RAGGED_SPLIT_MAX_BN ? RAGGED_MAX_SPLIT : 1;
+        for (int s = 1; s <= most && s <= blocks && s <= sms; s *= 2) {
+            if (is_pinned) {
+                if (!pinned || s == forced_split) {
+                    pinned = &k;
+                    *split = s;
+                }
+                continue;
+            }
+            const double us = ragged_estimate(k, s, groups, rows, N, K, sms);
+            if (!pinned && (!best || us < best_us)) {
+                best = &k;
+                best_us = us;
+                *split = s;
+            }
         }
     }
-    return best;
+    return pinned ? pinned : best;
 }
 
 int check_ragged(int dir, const void *A, const void *B, void *D, const int *offsets, int dtype, int G, int M_sum,
@@ -151,8 +173,9 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
         const size_t bytes = (size_t)G * N * K * (d_type == RAGGED_OUT_F32 ? 4 : 2);
         return cudaMemsetAsync(D, 0, bytes, stream) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
     }
-    // the result's type picks the kernel of a weight gradient
-    const RaggedKernel *k = choose_ragged(dir, G, M_sum, N, K, dev.sms);
+    int split = 1;
+    // (the result's type picks the kernel of a weight gradient)
+    const RaggedKernel *k = choose_ragged(dir, G, M_sum, N, K, dev.sms, &split);
     if (!k)
         return DG_ERR_UNSUPPORTED_SHAPE;
     const bool bf16 = dtype == DG_INPUT_BF16;
@@ -170,6 +193,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     p.total_rows = M_sum;
     p.out_type = d_type;
     p.accumulate = accumulate;
+    p.split = split;
     const int out = dir == RAGGED_NT ? N : K; // columns of the result
     const int red = dir == RAGGED_NT ? K : N; // reduction of NT, NN
     p.d_rows = N;
@@ -201,7 +225,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     const int slots = k->swap ? 0 : k->bn == 256 ? 1 : 2;
     int stages = RAGGED_MAX_STAGES;
     for (; stages >= 2; --stages) {
-        make_ragged_plan(p, stage, stages, slots);
+        make_ragged_plan(p, stage, stages, slots, split > 1 ? (uint32_t)k->bn * 512u : 0u);
         if ((int)p.total + 1024 <= dev.max_smem)
             break;
     }
@@ -258,9 +282,10 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     args.params = &p;
     args.device = dev.index;
     args.max_smem = dev.max_smem;
-    const long ctas = k->pair ? 2 * tiles : tiles;
-    const int sms = k->pair ? (dev.sms > 1 ? dev.sms / 2 * 2 : 2) : dev.sms;
-    args.grid = (int)(ctas < sms ? ctas : sms);
+    args.cluster = k->pair ? 2 : split;
+    const long ctas = tiles * args.cluster;
+    const long held = (long)clusters_held(args.cluster, dev.sms) * args.cluster;
+    args.grid = (int)(ctas < held ? ctas : held);
     args.smem_bytes = (int)p.total + 1024;
     args.stream = stream;
     return k->launch(args) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
@@ -424,15 +449,19 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
                : DG_ERR_CUDA;
 }
 
-int dg_force_ragged(int swap_ab, int cta_pair, int block_n)
+int dg_force_ragged(int swap_ab, int cta_pair, int block_n, int split)
 {
-    if (swap_ab == 0 && cta_pair == 0 && block_n == 0) {
+    if (swap_ab == 0 && cta_pair == 0 && block_n == 0 && split == 0) {
         g_forced_ragged.store(0, std::memory_order_relaxed);
         return DG_OK;
     }
+    const int most = swap_ab && block_n <= RAGGED_SPLIT_MAX_BN ? RAGGED_MAX_SPLIT : 1;
+    if (split < 0 || split > most || (split & (split - 1)) != 0)
+        return DG_ERR_UNSUPPORTED_SHAPE;
     for (int i = 0; i < kNumRagged; ++i)
         if (kRagged[i].swap == swap_ab && kRagged[i].pair == cta_pair && kRagged[i].bn == block_n) {
-            g_forced_ragged.store((uint32_t)block_n | (uint32_t)swap_ab << 16 | (uint32_t)cta_pair << 17,
+            g_forced_ragged.store((uint32_t)block_n | (uint32_t)swap_ab << 16 | (uint32_t)cta_pair << 17 |
+                                      (uint32_t)(split > 0 ? split : 1) << 20,
                                   std::memory_order_relaxed);
             return DG_OK;
         }

@@ -33,6 +33,7 @@ struct RaggedLaunchArgs {
     int device;
     int max_smem;
     int grid;
+    int cluster; // CTAs that share a tile
     int smem_bytes;
     cudaStream_t stream;
 };

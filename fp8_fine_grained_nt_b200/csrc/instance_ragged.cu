@@ -65,11 +65,11 @@ cudaError_t FP8NT_RAGGED_NAME(FP8NT_R_DIR, FP8NT_R_SWAP, FP8NT_R_PAIR, FP8NT_R_B
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = (unsigned)args.cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = FP8NT_R_PAIR ? 2 : 1;
+    cfg.numAttrs = args.cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, *args.tmap_x, *args.tmap_y, *args.tmap_d, *args.params);
 }
 

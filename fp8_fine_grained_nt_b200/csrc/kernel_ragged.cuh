@@ -27,6 +27,11 @@
 //   SWAP   the weights are X (128 of the output's columns per tile) and BN
 //          token rows are Y: for few rows per group, where the call is bound
 //          by reading the weights and 128 token rows would be mostly padding.
+//          Where there are too few such tiles to fill the SMs, the CTAs of a
+//          cluster share one: each sums a range of the reduction, sends every
+//          other CTA the part of its FP32 sums that the other one owns (token
+//          rows) through distributed shared memory, and adds up what it
+//          receives in rank order.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
@@ -153,6 +158,16 @@ __device__ __forceinline__ void drain_ragged(uint64_t *bar, uint32_t parity, vol
         wait_slow(a, parity, abort_flag, p.status, p.timeout_ns, false);
 }
 
+// The same for a barrier that other CTAs of the cluster arrive on after writing
+// this one's shared memory.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                             const RaggedParams &p)
+{
+    const bool got = wait_ragged(bar, parity, abort_flag, p);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return got;
+}
+
 // One operand's 64-wide reduction block: K-major, one box of ROWS rows of 128
 // bytes; MN-major, ROWS / 64 boxes of 64 reduction rows of 128 bytes.
 // GROUPED: the tensor has a group axis.  LEADER: completion is counted on the
@@ -210,6 +225,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     uint64_t *acc_full = tail_ready + RAGGED_MAX_STAGES;              // accumulator complete (x2)
     uint64_t *acc_empty = acc_full + 2;                               // accumulator read (x2)
     uint64_t *mma_done = acc_empty + 2;
+    uint64_t *recv_full = mma_done + 1; // split: every CTA's sums for this one's token rows are here
+    uint64_t *recv_free = recv_full + 1; // split: every CTA has read what this one sent
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + p.off_misc);
     volatile uint32_t *abort_flag = misc + 1;
     int *tiles = reinterpret_cast<int *>(smem + p.off_groups);
@@ -229,6 +246,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             mbar_init(&acc_empty[b], PAIR ? 16 : 8);
         }
         mbar_init(mma_done, 1);
+        mbar_init(recv_full, 4u * (uint32_t)p.split);
+        mbar_init(recv_free, 8u * (uint32_t)p.split);
         misc[1] = 0u;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmap_x);
@@ -294,16 +313,21 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         }
     }
     tc_fence_before();
-    if constexpr (PAIR)
-        cluster_sync(); // the peer may arrive on the leader's barriers from here on
+    const bool split = SWAP && p.split > 1;
+    if (PAIR || split)
+        cluster_sync(); // the others may arrive on this CTA's barriers from here on
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = misc[0];
     const int num_tiles = TN ? p.num_groups * (int)p.tiles_per_group.d : tiles[p.num_groups];
-    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-    const bool leader = rank == 0;
-    const int t_first = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
-    const int t_stride = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
+    const uint32_t rank = PAIR || split ? cluster_ctarank() : 0u;
+    const bool leader = !PAIR || rank == 0; // issues the MMAs
+    const int per_tile = PAIR ? 2 : SWAP ? p.split : 1; // CTAs that share a tile
+    const int t_first = (int)blockIdx.x / per_tile;
+    const int t_stride = (int)gridDim.x / per_tile;
+    // split: this CTA's range of the reduction
+    const int kb_first = SWAP ? (int)((long)p.nkb * rank / p.split) : 0;
+    const int kb_count = SWAP ? (int)((long)p.nkb * (rank + 1) / p.split) - kb_first : 0;
     int group = 0; // of the role's current tile
 
     if (warp == 0) {
@@ -320,8 +344,9 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                 const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
                 const int x_mn = ti.i0 + (PAIR ? (int)rank * 128 : 0) + ((!TN && !SWAP) ? ti.first : 0);
                 const int y_mn = ti.j0 + (PAIR ? (int)rank * T::Y_ROWS : 0) + (SWAP ? ti.first : 0);
-                const int red0 = TN ? ti.first : 0;
-                for (int kb = 0; kb < ti.nkb; ++kb) {
+                const int red0 = TN ? ti.first : kb_first * T::BK;
+                const int nkb = SWAP ? kb_count : ti.nkb;
+                for (int kb = 0; kb < nkb; ++kb) {
                     if (!wait_ragged(&empty[s], phase, abort_flag, p)) {
                         ok = false;
                         break;
@@ -386,12 +411,13 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             bool ok = true;
             for (int t = t_first; ok && t < num_tiles; t += t_stride) {
                 const RaggedTile ti = ragged_tile<DIR, SWAP, T::BM, BN, T::BK>(p, t, group, tiles, first, count);
-                if (ti.nkb == 0)
+                const int nkb = SWAP ? kb_count : ti.nkb;
+                if (nkb == 0)
                     continue;
                 uint32_t buf = tile_it & 1;
                 if (!wait_ragged(&acc_empty[buf], ((tile_it >> 1) & 1) ^ 1, abort_flag, p))
                     break;
-                for (int kb = 0; kb < ti.nkb; ++kb) {
+                for (int kb = 0; kb < nkb; ++kb) {
                     // FP32 results: a fresh accumulator for each partial sum
                     if (F32 && kb > 0 && kb % PARTIAL == 0) {
                         buf = ++tile_it & 1;
@@ -434,7 +460,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         mma_commit_pair_mc(&empty[s], 0x3);
                     else
                         mma_commit(&empty[s]);
-                    if (kb == ti.nkb - 1 || (F32 && kb % PARTIAL == PARTIAL - 1)) {
+                    if (kb == nkb - 1 || (F32 && kb % PARTIAL == PARTIAL - 1)) {
                         if constexpr (PAIR)
                             mma_commit_pair_mc(&acc_full[buf], 0x3);
                         else
@@ -598,6 +624,66 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             }
             const uint32_t taddr = taddr0 + buf * (uint32_t)BN;
             const int i0 = ti.i0 + (PAIR ? (int)rank * 128 : 0) + q * 32; // this warp's first X row
+            if constexpr (SWAP && BN <= RAGGED_SPLIT_MAX_BN) {
+                if (split) {
+                    const int tok_all = min(BN, ti.rows - ti.j0); // token rows of the tile,
+                    const int shift = __ffs(BN / p.split) - 1;
+                    const int own = 1 << shift; // of which every CTA owns so many
+                    float v[32];
+                    if constexpr (NC == 8)
+                        tmem_ld8p(taddr, v);
+                    else if constexpr (NC == 16)
+                        tmem_ld16(taddr, v);
+                    else
+                        tmem_ld32(taddr, v);
+                    tmem_wait_ld(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&acc_empty[buf]);
+                    // what was sent for the tile before has been read everywhere
+                    bool got = wait_ragged(recv_free, (tile_it & 1) ^ 1, abort_flag, p);
+                    if (!__all_sync(0xffffffffu, got))
+                        break;
+                    // received: [source][owned token row][128 columns]
+                    const uint32_t recv = smem_addr(smem + p.off_recv);
+                    const uint32_t mine = recv + (uint32_t)((rank * own * 128 + q * 32 + lane) * 4);
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) {
+                        const int tok = c_first + j;
+                        if (tok < tok_all) {
+                            const int to = tok >> shift;
+                            st_cluster_f32(map_shared_rank(mine + (uint32_t)((tok - to * own) * 512), (uint32_t)to),
+                                           v[j]);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int to = c_first >> shift; to < (c_first + NC) >> shift; ++to)
+                            mbar_arrive_cluster_release(map_shared_rank(smem_addr(recv_full), (uint32_t)to));
+                    got = wait_cluster(recv_full, tile_it & 1, abort_flag, p);
+                    if (!__all_sync(0xffffffffu, got))
+                        break;
+                    // the owned token rows: 256 threads, a column each, two rows at a time
+                    const int x = (int)threadIdx.x - 128;
+                    const int col = ti.i0 + (x & 127);
+                    for (int t0 = x >> 7; t0 < own; t0 += 2) {
+                        const int tok = (int)rank * own + t0;
+                        float sum = 0.0f;
+                        for (int z = 0; z < p.split; ++z)
+                            sum += ld_shared_f32(recv + (uint32_t)(((z * own + t0) * 128 + (x & 127)) * 4));
+                        if (tok < tok_all && col < p.d_cols)
+                            static_cast<uint16_t *>(p.d)[(size_t)(ti.first + ti.j0 + tok) * p.d_cols + col] =
+                                (uint16_t)pack_16x2(sum, 0.0f, bf16);
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int z = 0; z < p.split; ++z)
+                            mbar_arrive_cluster_release(map_shared_rank(smem_addr(recv_free), (uint32_t)z));
+                    ++tile_it;
+                    continue;
+                }
+            }
             if constexpr (SWAP) {
                 // a lane owns output column i0 + lane and the tile's token
                 // rows: 32 lanes store 64 consecutive bytes of a row
@@ -740,8 +826,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     }
 
     __syncwarp();
-    if constexpr (PAIR)
-        cluster_sync(); // neither CTA leaves while its pair may still use its memory
+    if (PAIR || split)
+        cluster_sync(); // no CTA leaves while another may still use its memory
     else
         __syncthreads();
     if (warp == 1) {

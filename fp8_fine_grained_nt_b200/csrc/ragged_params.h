@@ -27,6 +27,8 @@ constexpr int RAGGED_REGS_OTHER = 56;   // TN32: registers of warps 0-3 and of t
 constexpr int RAGGED_REGS_EPILOGUE = 224;
 static_assert(4 * 32 * RAGGED_REGS_OTHER + 8 * 32 * RAGGED_REGS_EPILOGUE <= RAGGED_THREADS * REGS_AT_LAUNCH,
               "register split exceeds the launch allocation");
+constexpr int RAGGED_SPLIT_MAX_BN = 64;  // swapped tiles that the CTAs of a cluster may share
+constexpr int RAGGED_MAX_SPLIT = 8;
 constexpr int RAGGED_MAX_STAGES = 12;
 constexpr int RAGGED_MAX_GROUPS = 1024;
 constexpr uint32_t RAGGED_SLOT_BYTES = 4096; // output staging: 32 rows of 128 bytes
@@ -66,24 +68,27 @@ struct RaggedParams {
     int out_type;        // RaggedOut
     int accumulate;      // TN32: add to the result
     uint32_t idesc;      // tcgen05.mma instruction descriptor
+    int split;           // SWAP: CTAs (a cluster) that share a tile's reduction; 1, 2, 4 or 8
     int stages;
     int out_slots;       // staging slots per epilogue warp (0 with SWAP)
     uint32_t off_out;
+    uint32_t off_recv;   // split: the sums received, BN token rows of 128 FP32 columns
     uint32_t off_groups; // tile prefix [G + 1], first row [G], rows [G]
     uint32_t off_bars;
     uint32_t off_misc;   // tensor-memory address, abort flag, scan partials
     uint32_t total;      // bytes, excluding the 1024-byte alignment slack
 };
 
-// Operand ring of `stages`, staging, group table, barriers.
-inline void make_ragged_plan(RaggedParams &p, uint32_t stage_bytes, int stages, int out_slots)
+// Operand ring of `stages`, staging, received sums, group table, barriers.
+inline void make_ragged_plan(RaggedParams &p, uint32_t stage_bytes, int stages, int out_slots, uint32_t recv_bytes)
 {
     p.stages = stages;
     p.out_slots = out_slots;
     p.off_out = stage_bytes * (uint32_t)stages;
-    p.off_groups = p.off_out + 8u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
+    p.off_recv = p.off_out + 8u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
+    p.off_groups = p.off_recv + recv_bytes;
     p.off_bars = align_up_u32(p.off_groups + 4u * (3u * (uint32_t)p.num_groups + 1u), 8);
-    p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 5u), 16);
+    p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 7u), 16);
     p.total = p.off_misc + 80;
 }
 

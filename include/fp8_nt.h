@@ -345,12 +345,13 @@ int dg_force_swap_ab(int mode);
 int dg_force_tail_split(int mode);
 
 /* Test hook: pin the tile form of later ragged grouped calls for which a
- * kernel of that form is built (0, 0, 0 = automatic choice): swap_ab 1 = the
+ * kernel of that form is built (0, 0, 0, 0 = automatic choice): swap_ab 1 = the
  * weights on the MMA's 128-row side and block_n (16, 32, 64 or 128) token rows
- * per tile; cta_pair 1 = 256 x 256 tiles by CTA pairs; block_n alone = one
- * CTA per tile of 128 x block_n.  Returns DG_ERR_UNSUPPORTED_SHAPE if no
- * direction has such a kernel. */
-int dg_force_ragged(int swap_ab, int cta_pair, int block_n);
+ * per tile, a tile's reduction shared by `split` CTAs (1, 2, 4 or 8 up to
+ * block_n 64, as far as the reduction allows; 0 = 1); cta_pair 1 = 256 x 256
+ * tiles by CTA pairs; block_n alone = one CTA per tile of 128 x block_n.
+ * Returns DG_ERR_UNSUPPORTED_SHAPE if no direction has such a kernel. */
+int dg_force_ragged(int swap_ab, int cta_pair, int block_n, int split);
 
 #ifdef __cplusplus
 }

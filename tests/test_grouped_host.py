@@ -104,9 +104,9 @@ def test_lora_sizes_and_refusals(lib):
 
 def test_force_ragged(lib):
     try:
-        for form in ((1, 0, 16), (1, 0, 32), (1, 0, 64), (1, 0, 128), (0, 1, 256), (0, 0, 256), (0, 0, 128), (0, 0, 0)):
+        for form in ((1, 0, 16, 8), (1, 0, 64, 4), (1, 0, 16), (1, 0, 32), (1, 0, 64), (1, 0, 128), (0, 1, 256), (0, 0, 256), (0, 0, 128), (0, 0, 0)):
             fp8.force_ragged(*form)
-        for form in ((1, 1, 256), (1, 0, 48), (0, 1, 128)):
+        for form in ((1, 1, 256), (1, 0, 48), (0, 1, 128), (1, 0, 128, 2), (1, 0, 16, 3), (0, 1, 256, 2)):
             with pytest.raises(fp8.Fp8NtError):
                 fp8.force_ragged(*form)
     finally:

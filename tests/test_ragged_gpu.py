@@ -17,7 +17,8 @@ import fp8_fine_grained_nt_b200 as fp8
 
 pytestmark = pytest.mark.gpu
 
-FORMS = {"auto": (0, 0, 0), "swap16": (1, 0, 16), "swap32": (1, 0, 32), "swap64": (1, 0, 64), "swap128": (1, 0, 128),
+FORMS = {"auto": (0, 0, 0), "swap16": (1, 0, 16), "swap32": (1, 0, 32), "swap64": (1, 0, 64),
+         "swap16_by_8": (1, 0, 16, 8), "swap32_by_2": (1, 0, 32, 2), "swap64_by_4": (1, 0, 64, 4), "swap128": (1, 0, 128),
          "single": (0, 0, 256), "pair": (0, 1, 256)}
 TN_FORMS = {"auto": (0, 0, 0), "single128": (0, 0, 128), "single256": (0, 0, 256), "pair": (0, 1, 256)}
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
@@ -59,7 +60,7 @@ def check(got, ref, mag, reduction):
 @pytest.fixture
 def form():
     yield lambda f: fp8.force_ragged(*f)
-    fp8.force_ragged(0, 0, 0)
+    fp8.force_ragged()
 
 
 def run_rows(direction, counts, N, K, dtype, seed=0, head=3, tail=5):
@@ -91,6 +92,16 @@ def run_rows(direction, counts, N, K, dtype, seed=0, head=3, tail=5):
 def test_rows_every_form(direction, name, counts, form):
     form(FORMS[name])
     run_rows(direction, COUNTS[counts], 264, 136, BF16)
+
+
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("bn", [16, 32, 64])
+@pytest.mark.parametrize("direction", ["nt", "nn"])
+def test_rows_shared_reductions(direction, bn, split, form):
+    """Tiles whose reduction a cluster shares, many tiles per cluster."""
+    form((1, 0, bn, split))
+    run_rows(direction, [5, 0, 70, 1, 33, 16], 1032, 1160, BF16, seed=split)
+    run_rows(direction, [1], 264, 2112, FP16, seed=split)
 
 
 @pytest.mark.parametrize("direction", ["nt", "nn"])
