@@ -60,6 +60,10 @@ int clusters_held(int together, int sms)
 //   NN  8 groups, N=7168, K=2048, 16 rows   58   36   38   44       51    55
 //                                128 rows       109   90   78       65    67
 //   NN 64 groups, N=2112, K=2048, 16 rows  104   87   92  108      102   137
+// and of BN = 16 shared by 1, 2, 4 and 8 CTAs:
+//   NT  1 group,  N=256,  K=7168, 10 rows   29   19   13    9
+//   NT 16 groups, N=4096, K=7168,  8 rows  145  144  144  171
+//   NT 64 groups, N=2112, K=2048,  8 rows   86  100  136  228
 //                                          128x128  128x256  pair
 //   TN 64 groups, N=2048, K=520, 64 rows        43       46    48
 //                              1024 rows       259      229   190
@@ -89,14 +93,15 @@ double ragged_estimate(const RaggedKernel &k, int split, int groups, int rows, i
     const double blocks = ceil(red / 64.0);
     const double mma = (k.swap ? 2.0 * (k.bn < 32 ? 32 : k.bn) : 512.0) + 152.0, load = stage / 61.0;
     // (sharing a tile takes an exchange of about 3000 cycles)
-    const double tile =
-        (ceil(blocks / split) * (mma > load ? mma : load) + 4670.0 + (split > 1 ? 3000.0 : 0.0)) / cycles_per_us;
+    const double fixed = k.swap ? split > 1 ? 7670.0 : 4670.0 : 7170.0;
+    const double tile = (ceil(blocks / split) * (mma > load ? mma : load) + fixed) / cycles_per_us;
     const double weights = 2.0 * wide * red / tok / 8.5e6; // read from memory for one tile
     const double power = 2.0 * tiles * bm * k.bn * blocks * 64.0 / 4.0e9; // all products, padding too
     const double full = floor(tiles / units), rest = tiles - full * units;
     const double wave = tile > units * weights ? tile : units * weights;
     const double last = rest <= 0 ? 0 : tile > rest * weights ? tile : rest * weights;
-    return full * wave + last + power;
+    // (a shared reduction has to be worth it: 5 %)
+    return (full * wave + last + power) * (split > 1 ? 1.05 : 1.0);
 }
 
 // The kernel of a call, and the CTAs that share a tile's reduction.

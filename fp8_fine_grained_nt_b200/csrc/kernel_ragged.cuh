@@ -658,28 +658,36 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0)
-                        for (int to = c_first >> shift; to < (c_first + NC) >> shift; ++to)
-                            mbar_arrive_cluster_release(map_shared_rank(smem_addr(recv_full), (uint32_t)to));
+                    if (lane < NC >> shift) // the owners of this warp's token rows
+                        mbar_arrive_cluster_release(
+                            map_shared_rank(smem_addr(recv_full), (uint32_t)((c_first >> shift) + lane)));
                     got = wait_cluster(recv_full, tile_it & 1, abort_flag, p);
                     if (!__all_sync(0xffffffffu, got))
                         break;
-                    // the owned token rows: 256 threads, a column each, two rows at a time
+                    // the owned token rows: 256 threads, a column each, every other
+                    // row.  The buffer is handed back before the stores: a
+                    // release would wait for them.
                     const int x = (int)threadIdx.x - 128;
                     const int col = ti.i0 + (x & 127);
-                    for (int t0 = x >> 7; t0 < own; t0 += 2) {
-                        const int tok = (int)rank * own + t0;
-                        float sum = 0.0f;
-                        for (int z = 0; z < p.split; ++z)
-                            sum += ld_shared_f32(recv + (uint32_t)(((z * own + t0) * 128 + (x & 127)) * 4));
-                        if (tok < tok_all && col < p.d_cols)
-                            static_cast<uint16_t *>(p.d)[(size_t)(ti.first + ti.j0 + tok) * p.d_cols + col] =
-                                (uint16_t)pack_16x2(sum, 0.0f, bf16);
+                    float sum[BN / 4];
+#pragma unroll
+                    for (int i = 0; i < BN / 4; ++i) {
+                        const int t0 = (x >> 7) + 2 * i;
+                        sum[i] = 0.0f;
+                        if (t0 < own)
+                            for (int z = 0; z < p.split; ++z)
+                                sum[i] += ld_shared_f32(recv + (uint32_t)(((z * own + t0) * 128 + (x & 127)) * 4));
                     }
                     __syncwarp();
-                    if (lane == 0)
-                        for (int z = 0; z < p.split; ++z)
-                            mbar_arrive_cluster_release(map_shared_rank(smem_addr(recv_free), (uint32_t)z));
+                    if (lane < p.split)
+                        mbar_arrive_cluster(map_shared_rank(smem_addr(recv_free), (uint32_t)lane));
+#pragma unroll
+                    for (int i = 0; i < BN / 4; ++i) {
+                        const int t0 = (x >> 7) + 2 * i, tok = (int)rank * own + t0;
+                        if (t0 < own && tok < tok_all && col < p.d_cols)
+                            static_cast<uint16_t *>(p.d)[(size_t)(ti.first + ti.j0 + tok) * p.d_cols + col] =
+                                (uint16_t)pack_16x2(sum[i], 0.0f, bf16);
+                    }
                     ++tile_it;
                     continue;
                 }
