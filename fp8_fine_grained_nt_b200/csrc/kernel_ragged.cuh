@@ -267,14 +267,15 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     // set itself up
     grid_dependency_wait();
     grid_launch_dependents();
-    // Segments, clamped into [0, total]; a bad offset is flagged.  Each
-    // thread takes `per` consecutive groups; exclusive prefix sums of their
-    // tiles by a block scan.
+    // Segments.  Each thread takes `per` consecutive groups; exclusive prefix
+    // sums of their tiles by a block scan.  A bad offset is flagged, and then
+    // one thread clamps every segment into the rows behind the one before it:
+    // segments that overlap would have more tiles than can be counted.
     {
         const int per = (p.num_groups + RAGGED_THREADS - 1) / RAGGED_THREADS;
         const int g0 = threadIdx.x * per;
         int mine = 0;
-        bool bad = false;
+        int bad = 0;
         for (int g = g0; g < min(g0 + per, p.num_groups); ++g) {
             const int lo = __ldg(p.offsets + g), hi = __ldg(p.offsets + g + 1);
             const int a = min(max(lo, 0), p.total_rows);
@@ -282,14 +283,23 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
             bad |= lo != a || hi != b;
             first[g] = a;
             count[g] = b - a;
-            if (!TN) {
-                constexpr int TOK = SWAP ? BN : T::BM;
-                mine += (b - a + TOK - 1) / TOK * (SWAP ? p.x_blocks : p.y_blocks);
-            }
         }
-        if (bad)
-            atomicOr(p.status, DEVERR_BAD_INDEX);
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0) {
+                atomicOr(p.status, DEVERR_BAD_INDEX);
+                for (int g = 0, at = 0; g < p.num_groups; ++g) {
+                    first[g] = min(max(__ldg(p.offsets + g), at), p.total_rows);
+                    at = min(max(__ldg(p.offsets + g + 1), first[g]), p.total_rows);
+                    count[g] = at - first[g];
+                }
+            }
+            __syncthreads();
+        }
         if (!TN) {
+            for (int g = g0; g < min(g0 + per, p.num_groups); ++g) {
+                constexpr int TOK = SWAP ? BN : T::BM;
+                mine += (count[g] + TOK - 1) / TOK * (SWAP ? p.x_blocks : p.y_blocks);
+            }
             int incl = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {

@@ -148,7 +148,7 @@ int quantize_fp8_1x128(const void *x, int x_dtype, void *q, float *sa, int M, in
  *   offsets  [num_groups + 1] int32 on the device (4-byte aligned; never read
  *            by the host), ascending, within [0, M_sum].  A value that is not
  *            sets DG_ERR_DEVICE_BAD_INDEX and is clamped to [0, M_sum] and to
- *            the segment's start.
+ *            the end of the segment before it.
  * Everything row-major and dense; N % 8 == 0, K % 8 == 0 (16-byte rows),
  * 1 <= num_groups <= 1024, 0 <= M_sum <= 0x7fff0000.  Sums are FP32 over the whole
  * reduction, rounded once (to nearest even) to D's type.  D must not overlap

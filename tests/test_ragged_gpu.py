@@ -219,13 +219,31 @@ def test_bad_offsets_are_flagged_and_clamped():
     d = torch.full((64, 128), 7.0, dtype=BF16, device="cuda")
     fp8.m_grouped_gemm_nt_ragged(a, b, d, torch.tensor([-4, 20, 10, 900], dtype=torch.int32, device="cuda"))
     assert fp8.get_device_status() == 7
-    # group 0: rows 0..19; group 1: empty (its end lies before its start); group 2: rows 10..63
+    # group 0: rows 0..19; group 1: empty (its end lies before its start); group 2: rows 20..63
     ref = a[20:].double() @ b[2].double().T
     check(d[20:], ref, a[20:].double().abs() @ b[2].double().abs().T, 128)
     g = torch.full((3, 128, 128), 7.0, dtype=FP32, device="cuda")
     fp8.k_grouped_gemm_tn_ragged(a, a, g, torch.tensor([0, 30, 30, 65], dtype=torch.int32, device="cuda"))
     assert fp8.get_device_status() == 7
     check(g[2], a[30:].double().T @ a[30:].double(), a[30:].double().abs().T @ a[30:].double().abs(), 34)
+
+
+def test_bad_offsets_do_not_overlap():
+    a, b = gen(128, 64, seed=7, dtype=BF16), gen(4, 64, 64, seed=8, dtype=BF16)
+    offsets = torch.tensor([0, 100, 40, 120, 90], dtype=torch.int32, device="cuda")
+    d = torch.full((128, 64), 7.0, dtype=BF16, device="cuda")
+    w = torch.full((4, 64, 64), 7.0, dtype=FP32, device="cuda")
+    bounds = [(0, 100), (100, 100), (100, 120), (120, 120)]
+    fp8.m_grouped_gemm_nt_ragged(a, b, d, offsets)
+    assert fp8.get_device_status() == 7
+    for g, (lo, hi) in enumerate(bounds):
+        check(d[lo:hi], a[lo:hi].double() @ b[g].double().T, a[lo:hi].double().abs() @ b[g].double().abs().T, 64)
+    assert (d[120:] == 7).all()
+    fp8.k_grouped_gemm_tn_ragged(a, a, w, offsets)
+    assert fp8.get_device_status() == 7
+    for g, (lo, hi) in enumerate(bounds):
+        x = a[lo:hi].double()
+        check(w[g], x.T @ x, x.abs().T @ x.abs(), hi - lo)
 
 
 def test_no_rows():
