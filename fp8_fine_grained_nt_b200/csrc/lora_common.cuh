@@ -63,8 +63,8 @@ __device__ __forceinline__ Slot read_slot(const LoraParams &p, int i)
     if (i < p.slots) {
         const int g = __ldg(p.m_indices + i);
         const int t = p.order ? __ldg(p.order + i) : i;
-        if (g >= 0 && t >= 0) {
-            if (g < p.adapters && t < p.rows) {
+        if (g != -1 && t != -1) {
+            if (g >= 0 && g < p.adapters && t >= 0 && t < p.rows) {
                 s.row = t;
                 s.adapter = g;
             } else {

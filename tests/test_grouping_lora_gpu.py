@@ -259,6 +259,20 @@ def test_lora_bad_slots_are_flagged_and_skipped():
         lora_check(d[2:3], x[2:3], A[1], B[1], 1.0, c[2:3])
 
 
+@pytest.mark.parametrize("T", [5, 400])
+def test_lora_negative_slots(T):
+    x, A, B = gen(T, 64, seed=1, dtype=BF16), gen(2, 8, 64, seed=2, dtype=BF16), gen(2, 64, 8, seed=3, dtype=BF16)
+    scale, c = torch.ones(2, device="cuda"), gen(T, 64, seed=4, dtype=BF16)
+    ids = torch.ones(T, dtype=torch.int32, device="cuda")
+    order = torch.arange(T, dtype=torch.int32, device="cuda")
+    for bad_ids, bad_order, status in ((-1, 3, 0), (-2, 3, 7), (1, -1, 0), (1, -2, 7)):
+        ids[3], order[3] = bad_ids, bad_order
+        d = torch.full_like(c, 9.0)
+        fp8.m_grouped_lora_add(x, A, B, scale, c, d, ids, order)
+        assert fp8.get_device_status() == status
+        assert (d[3] == 9).all() and not (d[4] == 9).all()
+
+
 def test_lora_no_slots():
     x, c = gen(4, 64, seed=1, dtype=BF16), gen(4, 64, seed=2, dtype=BF16)
     A, B = gen(2, 8, 64, seed=3, dtype=BF16), gen(2, 64, 8, seed=4, dtype=BF16)
