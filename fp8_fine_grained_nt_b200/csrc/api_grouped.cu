@@ -33,6 +33,7 @@ std::atomic<uint32_t> g_forced_ragged{0};
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
+constexpr int kMaxSize = 0x7fff0000; // rows of a product, N and K: 32-bit coordinates, with room for the last tile
 constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, with room to round up
 
 // Clusters of `together` CTAs, one CTA per SM, that run at once on `sms` SMs:
@@ -149,9 +150,9 @@ int check_ragged(int dir, const void *A, const void *B, void *D, const int *offs
     // bytes of one group's weights: the stride of a tensor map's group axis
     if ((uint64_t)N * (uint64_t)K * 4u >= (1ull << 40))
         return DG_ERR_UNSUPPORTED_SHAPE;
-    // rows are 32-bit coordinates, with room for the last tile, and the tiles of
-    // the smallest tile form are counted in 32 bits
-    if (M_sum > 0x7fff0000 || (ceil_div(M_sum, 16) + G) * ceil_div(N > K ? N : K, 128) > 0x7fffffffL ||
+    // the tiles of the smallest tile form are counted in 32 bits
+    if (M_sum > kMaxSize || N > kMaxSize || K > kMaxSize ||
+        (ceil_div(M_sum, 16) + G) * ceil_div(N > K ? N : K, 128) > 0x7fffffffL ||
         (long)G * ceil_div(N, 128) * ceil_div(K, 128) > 0x7fffffffL)
         return DG_ERR_UNSUPPORTED_SHAPE;
     // without rows only the weight gradient has anything to write
@@ -332,8 +333,8 @@ int k_grouped_gemm_tn_ragged(const void *A, const void *B, void *D, const int *o
     // that a sum over many calls is not rounded to 16 bits at each
     if ((d_dtype != DG_INPUT_F32 && d_dtype != dtype) || (accumulate && d_dtype != DG_INPUT_F32))
         return DG_ERR_INVALID_ARGUMENT;
-    return run_ragged(d_dtype == DG_INPUT_F32 ? RAGGED_TN32 : RAGGED_TN, A, B, D, offsets, dtype, d_dtype, accumulate != 0, num_groups, M_sum, N, K,
-                      reinterpret_cast<cudaStream_t>(stream));
+    return run_ragged(d_dtype == DG_INPUT_F32 ? RAGGED_TN32 : RAGGED_TN, A, B, D, offsets, dtype, d_dtype,
+                      accumulate != 0, num_groups, M_sum, N, K, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int get_row_groups_capacity(int num_rows, int num_groups, int alignment)
@@ -389,7 +390,7 @@ long long get_lora_workspace_size(int num_slots, int num_adapters, int rank, int
     if (num_slots < 0 || num_adapters <= 0 || rank < 0 || N < 0 || K < 0)
         return -DG_ERR_INVALID_ARGUMENT;
     if (num_slots > kMaxSlots || rank == 0 || rank > LORA_MAX_RANK || rank % 8 != 0 || N == 0 || N % 8 != 0 || K == 0 ||
-        K % 8 != 0)
+        K % 8 != 0 || N > kMaxSize || K > kMaxSize)
         return -DG_ERR_UNSUPPORTED_SHAPE;
     if (num_slots == 0 || lora_is_wide(num_slots, num_adapters, rank))
         return 0;

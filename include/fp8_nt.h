@@ -150,8 +150,8 @@ int quantize_fp8_1x128(const void *x, int x_dtype, void *q, float *sa, int M, in
  *            sets DG_ERR_DEVICE_BAD_INDEX and is clamped to [0, M_sum] and to
  *            the end of the segment before it.
  * Everything row-major and dense; N % 8 == 0, K % 8 == 0 (16-byte rows),
- * 1 <= num_groups <= 1024, 0 <= M_sum <= 0x7fff0000.  Sums are FP32 over the whole
- * reduction, rounded once (to nearest even) to D's type.  D must not overlap
+ * 1 <= num_groups <= 1024; M_sum, N and K <= 0x7fff0000.  Sums are FP32 over the
+ * whole reduction, rounded once (to nearest even) to D's type.  D must not overlap
  * A or B. */
 
 /* Forward: D[t,n] = sum_k A[t,k] * B[g,n,k] for t in segment g.
@@ -229,7 +229,7 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups);
  *             group_rows_by_index orders them) share the reads of its weights.
  * A value out of range sets DG_ERR_DEVICE_BAD_INDEX and its slot is skipped.
  * rank: a multiple of 8, at most 256 (smaller adapters: zero rows of A and
- * columns of B); N % 8 == 0, K % 8 == 0.  workspace: at least
+ * columns of B); N % 8 == 0, K % 8 == 0, both <= 0x7fff0000.  workspace: at least
  * get_lora_workspace_size(num_slots, num_adapters, rank, N, K) bytes (0 for
  * long batches), 16-byte aligned, in use until the call's work has completed;
  * calls that may run at the same time need one each. */

@@ -33,6 +33,8 @@ def test_ragged_rows_refusals(lib, name):
     assert f(P, P, P, P, BF16, 1024, 64, 1 << 20, 1 << 20, None) == 3   # a group's weights over 2^40 bytes
     assert f(P, P, P, P, BF16, 1024, 2 ** 30, 1 << 18, 64, None) == 3      # tiles over 2^31
     assert f(P, P, P, P, BF16, 4, 2 ** 31 - 1, 64, 64, None) == 3          # rows
+    assert f(P, P, P, P, BF16, 1, 16, 2 ** 31 - 8, 8, None) == 3           # columns
+    assert f(P, P, P, P, BF16, 1, 16, 8, 2 ** 31 - 8, None) == 3
     for bad in range(4):
         args = [P] * 4
         args[bad] = NULL
@@ -100,6 +102,12 @@ def test_lora_sizes_and_refusals(lib):
     assert call(size=0) == 1 and call(ws=NULL) == 1 and call(m=NULL) == 1 and call(s=NULL) == 1 and call(d=NULL) == 1
     assert call(x=MIS) == 2 and call(a=MIS) == 2 and call(b=MIS) == 2 and call(c=MIS) == 2 and call(ws=MIS) == 2
     assert call(m=ctypes.c_void_p(0x10002)) == 2
+
+
+def test_lora_columns_near_2_to_31(lib):
+    assert lib.get_lora_workspace_size(1, 1, 8, 2 ** 31 - 8, 64) == -3
+    assert lib.get_lora_workspace_size(1, 1, 8, 64, 2 ** 31 - 8) == -3
+    assert lib.get_lora_workspace_size(1, 1, 8, 0x7fff0000, 64) > 0
 
 
 def test_force_ragged(lib):
