@@ -120,6 +120,8 @@ const RaggedKernel *choose_ragged(int dir, int groups, int rows, int N, int K, i
             continue;
         const bool is_pinned =
             ((uint32_t)k.bn | (uint32_t)k.swap << 16 | (uint32_t)k.pair << 17) == (forced & 0xFFFFFu);
+        if (k.pair && sms < 2 && !is_pinned) // (a bound on the SMs may leave no room for a pair)
+            continue;
         const int most = k.swap && k.bn <= RAGGED_SPLIT_MAX_BN ? RAGGED_MAX_SPLIT : 1;
         for (int s = 1; s <= most && s <= blocks && s <= sms; s *= 2) {
             if (is_pinned) {

@@ -194,7 +194,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (n != N)
         return PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
     try {
-        return PyLong_FromLongLong(F(args));
+        const long long status = F(args);
+        return PyErr_Occurred() ? nullptr : PyLong_FromLongLong(status); // (an argument's own error)
     } catch (const std::exception &e) { // e.g. no memory for the workspace
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;

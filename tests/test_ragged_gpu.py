@@ -394,3 +394,10 @@ def test_refusals_of_device_tensors():
     with pytest.raises(TypeError):
         fp8.k_grouped_gemm_tn_ragged(a, d, w.half(), off)
     assert fp8.get_device_status() == 0
+
+
+def test_error_of_an_argument_itself():
+    a, w = gen(16, 64, seed=1, dtype=BF16), torch.zeros(1, 64, 64, device="cuda")
+    offsets = torch.tensor([0, 16], dtype=torch.int32, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        fp8.k_grouped_gemm_tn_ragged(a, a, w, offsets, accumulate=torch.zeros(2))
