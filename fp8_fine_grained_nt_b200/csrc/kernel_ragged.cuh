@@ -15,8 +15,9 @@
 // zero, a bias that grows with the length: nothing beside the rounding to 16
 // bits, but 4e-6 of an FP32 weight gradient over 2048 rows (and 3e-5 over
 // 16384).  So FP32 results (direction TN32) are added up in registers, rounded
-// to nearest, from partial sums of 512 rows: 5e-7, for 7 % of the time (477 -> 510 us at 16384
-// rows, N = 7168, K = 2048; partial sums of 256 rows cost 15 %).
+// to nearest, from partial sums of 512 rows: 5e-7, for 7 % of the time (477 ->
+// 510 us at 16384 rows, N = 7168, K = 2048, with stages of 64 rows; partial
+// sums of 256 rows cost 15 %).
 //
 // Tile forms:
 //   PAIR   256 x 256 by a cluster of two CTAs (cta_group::2): each CTA loads
@@ -33,12 +34,18 @@
 //          rows) through distributed shared memory, and adds up what it
 //          receives in rank order.
 //
+// Long groups are bound by the tensor core: 8192 x 8192 x 8192 takes 711 us,
+// 1546 TFLOP/s (a library product of that size: 1613); back to back the power
+// limit holds both near 1370.  Few rows per group are bound by reading the
+// weights: 128 rows over 16 groups, N = 4096, K = 7168, 155 us, 6.1 TB/s.
+// Weight gradients of short groups are bound by their epilogue: 1999 rows over
+// 64 groups, 2048 x 520 into BF16, 44 us, 3.3 TB/s.
+//
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
 // only), warps 4-11 epilogue (a 32-lane quarter of tensor memory and half of the
-// tile's columns each).  Two
-// accumulators in tensor memory let a tile's epilogue overlap the next
-// tile's MMAs.
+// tile's columns each).  Two accumulators in tensor memory let a tile's
+// epilogue overlap the next tile's MMAs.
 #pragma once
 
 #include "kernel.cuh"
