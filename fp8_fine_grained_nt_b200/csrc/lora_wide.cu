@@ -61,12 +61,13 @@ constexpr uint32_t WIDE_C_BYTES = WIDE_SLOTS * 256; // 128 slots x 128 columns
 struct WidePlan {
     int cluster;
     int segs;        // adapters per pass
-    int stages2;
+    int stages2;     // of the B ring, two of which lie in the first ring's room
     uint32_t a_bytes; // 64 of k of one adapter's A
     uint32_t ring;    // bytes of the first ring: as many stages as a pass's adapters allow
     uint32_t off_c;     // two c buffers in the region of the first ring: behind the exchanged shares, or in their place
     uint32_t off_v;     // hi, lo: [2][rank chunk][128][128 B]
-    uint32_t off_b;     // B ring
+    uint32_t off_b;     // B ring but for its last two stages
+    uint32_t off_b2;    // those: behind the c buffers, free once phase 1 is done
     uint32_t off_bars;
     uint32_t total;
 };
@@ -226,12 +227,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
         };
         auto parity1 = [&](const Ring &r) { return ((phase1 >> r.s) ^ r.odd) & 1u; };
+        auto b_at = [&](uint32_t s) {
+            return s + 2 < s2 ? plan.off_b + s * WIDE_B_BYTES : plan.off_b2 + (s + 2 - s2) * WIDE_B_BYTES;
+        };
         auto load_b = [&](int t, int i, int rc) { // stage it2 of the B ring
             const uint32_t s = it2 % s2; // (of the B ring)
             if (!ok || !(ok = wait(&empty2[s], ((it2 / s2) & 1) ^ 1)))
                 return;
             mbar_arrive_expect_tx(&full2[s], WIDE_B_BYTES);
-            tma_load_nd<true, false>(smem + plan.off_b + s * WIDE_B_BYTES, &tmap_b, smem_addr(&full2[s]), rc * 64,
+            tma_load_nd<true, false>(smem + b_at(s), &tmap_b, smem_addr(&full2[s]), rc * 64,
                                      (t * cl + rank) * 128, seg_adapter[seg0 + i]);
             ++it2;
         };
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const uint32_t dst = (uint32_t)((warp * 32 + (lane >> 3)) * 128);
             // a stage is published once its copies have landed, `lag` rounds
             // after they were issued
-            const int lag = s1 >= 6 ? 4 : 2; // less than the stages there are
+            const int lag = s1 >= 6 ? 4 : s1 >= 4 ? 3 : 2; // less than the stages there are
             Ring at = {0, s1, 0u}, behind = {0, s1, 0u};
             auto publish = [&]() {
                 fence_proxy_async_smem();
@@ -287,6 +291,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (i >= lag) {
                     if (lag == 4)
                         cp_async_wait<4>();
+                    else if (lag == 3)
+                        cp_async_wait<3>();
                     else
                         cp_async_wait<2>();
                     publish();
@@ -308,8 +314,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                                                  smem_addr(&full1[s]), (i * cl + rank) * 64, 0,
                                                  seg_adapter[seg0 + j]);
                 }
-                // the first stages of B, while the products of phase 1 run
-                for (; b_done < min(b_loads, (int)s2); ++b_done)
+                // the first stages of B that have their own room, while the
+                // products of phase 1 run
+                for (; ok && b_done < b_loads && it2 % s2 + 2 < s2; ++b_done)
                     load_b(b_done / (segs * chunks), b_done / chunks % segs, b_done % chunks);
             }
         } else if (warp == 4) {
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     for (int i = 0; ok && i < segs;) {
                         const uint32_t d = tmem + (buf * segs + i) * 128;
                         // two adapters at once where their B lies side by side
-                        const int both = it2 % s2 == 0 && chunks == 1 && i + 1 < segs ? 2 : 1;
+                        const int both = it2 % 2 == 0 && chunks == 1 && i + 1 < segs ? 2 : 1;
                         const uint32_t idesc2 = wp.idesc | (uint32_t)(both * 128 >> 3) << 17;
                         for (int rc = 0; ok && rc < chunks; ++rc, it2 += both) {
                             const uint32_t s = it2 % s2;
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                             if (!ok)
                                 break;
                             tc_fence_after();
-                            const uint64_t bd = make_sdesc(base + plan.off_b + s * WIDE_B_BYTES);
+                            const uint64_t bd = make_sdesc(base + b_at(s));
                             const int steps = min(4, (p.R - rc * 64 + 15) / 16);
 #pragma unroll
                             for (int term = 0; term < 2; ++term) {
@@ -622,8 +629,12 @@ WidePlan wide_plan(int slots, int R)
     w.off_c = R <= 64 ? align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024) : 0;
     w.off_v = w.ring;
     w.off_b = w.off_v + 2 * chunks * WIDE_X_BYTES;
-    w.stages2 = R <= 64 ? 2 : 3;
-    w.off_bars = w.off_b + (uint32_t)w.stages2 * WIDE_B_BYTES;
+    // two adapters' tiles take two stages of B: with only those, the next tile's
+    // came after its products (45 -> 42 us for 4096 rows of 8 adapters)
+    const uint32_t own = R <= 64 ? 2 : 3;
+    w.stages2 = (int)own + 2;
+    w.off_b2 = w.off_c + 2 * WIDE_C_BYTES;
+    w.off_bars = w.off_b + own * WIDE_B_BYTES;
     w.total = w.off_bars + 8u * (4u * WIDE_MAX_STAGES + 6u);
     return w;
 }
