@@ -61,13 +61,13 @@ constexpr uint32_t WIDE_C_BYTES = WIDE_SLOTS * 256; // 128 slots x 128 columns
 struct WidePlan {
     int cluster;
     int segs;        // adapters per pass
-    int stages2;     // of the B ring, two of which lie in the first ring's room
+    int stages2;     // of the B ring
     uint32_t a_bytes; // 64 of k of one adapter's A
     uint32_t ring;    // bytes of the first ring: as many stages as a pass's adapters allow
-    uint32_t off_c;     // two c buffers in the region of the first ring: behind the exchanged shares, or in their place
-    uint32_t off_v;     // hi, lo: [2][rank chunk][128][128 B]
-    uint32_t off_b;     // B ring but for its last two stages
-    uint32_t off_b2;    // those: behind the c buffers, free once phase 1 is done
+    // in the room of the first ring, once phase 1 is done: the exchanged shares, and
+    uint32_t off_c; // two c buffers: behind the shares, or in their place
+    uint32_t off_v; // hi, lo: [2][rank chunk][128][128 B]
+    uint32_t off_b; // B ring
     uint32_t off_bars;
     uint32_t total;
 };
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const int segs = min(plan.segs, total_segs - seg0);
         const uint32_t stage_bytes = WIDE_X_BYTES + (uint32_t)segs * plan.a_bytes; // 64 of k
         const int kbs = ((p.K + 63) / 64 - rank + cl - 1) / cl;
-        const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 3
+        const int s1 = min(WIDE_MAX_STAGES, (int)(plan.ring / stage_bytes)); // at least 4
         // a walk along the first ring: stage, and which of its uses in this pass is odd
         struct Ring {
             int s, stages;
@@ -227,15 +227,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
         };
         auto parity1 = [&](const Ring &r) { return ((phase1 >> r.s) ^ r.odd) & 1u; };
-        auto b_at = [&](uint32_t s) {
-            return s + 2 < s2 ? plan.off_b + s * WIDE_B_BYTES : plan.off_b2 + (s + 2 - s2) * WIDE_B_BYTES;
-        };
         auto load_b = [&](int t, int i, int rc) { // stage it2 of the B ring
             const uint32_t s = it2 % s2; // (of the B ring)
             if (!ok || !(ok = wait(&empty2[s], ((it2 / s2) & 1) ^ 1)))
                 return;
             mbar_arrive_expect_tx(&full2[s], WIDE_B_BYTES);
-            tma_load_nd<true, false>(smem + b_at(s), &tmap_b, smem_addr(&full2[s]), rc * 64,
+            tma_load_nd<true, false>(smem + plan.off_b + s * WIDE_B_BYTES, &tmap_b, smem_addr(&full2[s]), rc * 64,
                                      (t * cl + rank) * 128, seg_adapter[seg0 + i]);
             ++it2;
         };
@@ -263,7 +260,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const uint32_t dst = (uint32_t)((warp * 32 + (lane >> 3)) * 128);
             // a stage is published once its copies have landed, `lag` rounds
             // after they were issued
-            const int lag = s1 >= 6 ? 4 : s1 >= 4 ? 3 : 2; // less than the stages there are
+            const int lag = s1 >= 6 ? s1 - 2 : 3; // less than the stages there are
             Ring at = {0, s1, 0u}, behind = {0, s1, 0u};
             auto publish = [&]() {
                 fence_proxy_async_smem();
@@ -289,12 +286,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 cp_async_commit();
                 if (i >= lag) {
-                    if (lag == 4)
+                    if (lag == 6)
+                        cp_async_wait<6>();
+                    else if (lag == 5)
+                        cp_async_wait<5>();
+                    else if (lag == 4)
                         cp_async_wait<4>();
-                    else if (lag == 3)
-                        cp_async_wait<3>();
                     else
-                        cp_async_wait<2>();
+                        cp_async_wait<3>();
                     publish();
                 }
             }
@@ -314,9 +313,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                                                  smem_addr(&full1[s]), (i * cl + rank) * 64, 0,
                                                  seg_adapter[seg0 + j]);
                 }
-                // the first stages of B that have their own room, while the
-                // products of phase 1 run
-                for (; ok && b_done < b_loads && it2 % s2 + 2 < s2; ++b_done)
+                // the first stages of B, during the exchange
+                ok = ok && wait(p1_done, pass_it & 1);
+                for (; ok && b_done < min(b_loads, (int)s2); ++b_done)
                     load_b(b_done / (segs * chunks), b_done / chunks % segs, b_done % chunks);
             }
         } else if (warp == 4) {
@@ -491,7 +490,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                             if (!ok)
                                 break;
                             tc_fence_after();
-                            const uint64_t bd = make_sdesc(base + b_at(s));
+                            const uint64_t bd = make_sdesc(base + plan.off_b + s * WIDE_B_BYTES);
                             const int steps = min(4, (p.R - rc * 64 + 15) / 16);
 #pragma unroll
                             for (int term = 0; term < 2; ++term) {
@@ -622,19 +621,20 @@ WidePlan wide_plan(int slots, int R)
     const uint32_t chunks = (uint32_t)(R + 63) / 64;
     w.segs = R <= 64 ? 4 : 1;
     w.a_bytes = (uint32_t)(R + 15) / 16 * 16 * 128;
-    // six stages of 64 of k with one adapter up to rank 64, at least three with
-    // four, or with one above; the shares (at most 68 KB) and two c buffers (64
-    // KB, beside the shares up to rank 64) in the same room
-    w.ring = R <= 64 ? 3u * 49152u : 98304u;
-    w.off_c = R <= 64 ? align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024) : 0;
-    w.off_v = w.ring;
+    // Phase 1 waits for memory (about 2.6 us a round trip under load), so its ring
+    // has all the room: eight stages of 64 of k with one adapter up to rank 64,
+    // six with two, or with one above, four with four.  Of phase 2, the c buffers
+    // lie behind the shares up to rank 64, else in their place.
+    const uint32_t shares = align_up_u32((uint32_t)WIDE_SLOTS * (uint32_t)(R + 4) * 4u, 1024);
+    w.off_c = R <= 64 ? shares : 0;
+    w.off_v = w.off_c + 2 * WIDE_C_BYTES > shares ? w.off_c + 2 * WIDE_C_BYTES : shares;
     w.off_b = w.off_v + 2 * chunks * WIDE_X_BYTES;
-    // two adapters' tiles take two stages of B: with only those, the next tile's
-    // came after its products (45 -> 42 us for 4096 rows of 8 adapters)
-    const uint32_t own = R <= 64 ? 2 : 3;
-    w.stages2 = (int)own + 2;
-    w.off_b2 = w.off_c + 2 * WIDE_C_BYTES;
-    w.off_bars = w.off_b + own * WIDE_B_BYTES;
+    // two adapters' tiles take two stages of B, the next tile's two more
+    w.stages2 = R <= 64 ? 4 : 5;
+    w.ring = w.off_b + (uint32_t)w.stages2 * WIDE_B_BYTES;
+    const uint32_t least = 4u * (WIDE_X_BYTES + 4u * 64u * 128u); // four stages of four adapters of rank 64
+    w.ring = w.ring > least ? w.ring : least;
+    w.off_bars = w.ring;
     w.total = w.off_bars + 8u * (4u * WIDE_MAX_STAGES + 6u);
     return w;
 }
