@@ -93,6 +93,20 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// At most n, up to 6, of the thread's groups are still on their way.
+__device__ __forceinline__ void cp_async_wait_for(int n)
+{
+    switch (n) {
+    case 0: cp_async_wait<0>(); break;
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 4: cp_async_wait<4>(); break;
+    case 5: cp_async_wait<5>(); break;
+    default: cp_async_wait<6>(); break;
+    }
+}
+
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
 {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -182,8 +196,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         slot_seg[tid] = mine.adapter >= 0 ? seg : -1;
         if (starts)
             seg_adapter[seg] = mine.adapter;
-        adapter_scale[tid] = mine.adapter >= 0 ? __ldg(p.scales + mine.adapter) : 0.0f;
     }
+    // (needed in the exchange)
+    const float scale = mine.adapter >= 0 ? __ldg(p.scales + mine.adapter) : 0.0f;
     tc_fence_before();
     cluster_arrive_relaxed(); // (all of the cluster runs before any shared memory of another CTA is touched)
     __syncthreads();
@@ -286,20 +301,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 cp_async_commit();
                 if (i >= lag) {
-                    if (lag == 6)
-                        cp_async_wait<6>();
-                    else if (lag == 5)
-                        cp_async_wait<5>();
-                    else if (lag == 4)
-                        cp_async_wait<4>();
-                    else
-                        cp_async_wait<3>();
+                    cp_async_wait_for(lag);
                     publish();
                 }
             }
-            cp_async_wait<0>();
-            for (int i = min(lag, kbs); ok && i > 0; --i)
+            for (int i = min(lag, kbs); ok && i > 0; --i) {
+                cp_async_wait_for(i - 1);
                 publish();
+            }
+            cp_async_wait<0>();
+            adapter_scale[tid] = scale; // (read in the exchange)
         } else if (warp == 5) {
             if (lane == 0) {
                 Ring at = {0, s1, 0u};
@@ -404,9 +415,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             cp_async_commit();
         };
         const bool early = plan.off_c > 0;
+        cluster_arrive(); // before the copies of c: a release would wait for them, 2 us
         if (early && warp >= 8 && n_tiles > 0)
             fetch_c(0);
-        cluster_sync(); // every CTA's share is there
+        cluster_wait(); // every CTA's share is there
         // this CTA's part of the slots, two per round of a warp
         const int part = WIDE_SLOTS / cl;
         for (int i = warp; i < part; i += 2 * WIDE_WARPS) {
@@ -437,17 +449,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     sum.z += v[h][z].z;
                     sum.w += v[h][z].w;
                 }
-                float scale = 1.0f;
+                float power = 1.0f;
                 if constexpr (!BF16)
-                    scale = lora_fp16_scale(
+                    power = lora_fp16_scale(
                         fmaxf(fmaxf(fabsf(sum.x), fabsf(sum.y)), fmaxf(fabsf(sum.z), fabsf(sum.w))));
-                const float inv = 1.0f / scale; // a power of two: exact
+                const float inv = 1.0f / power; // a power of two: exact
                 uint32_t hi[2], lo[2];
                 split_two<BF16>(sum.x * inv, sum.y * inv, hi[0], lo[0]);
                 split_two<BF16>(sum.z * inv, sum.w * inv, hi[1], lo[1]);
                 const uint32_t at = base + plan.off_v + (uint32_t)((rk >> 6) * WIDE_X_BYTES + r[h] * 128 +
                                                                    ((((rk & 63) >> 3) ^ (r[h] & 7)) << 4) + (rk & 7) * 2);
-                const float f = scale * adapter_scale[r[h]];
+                const float f = power * adapter_scale[r[h]];
                 for (int z = 0; z < cl; ++z) {
                     if (rk < chunks * 64) {
                         const uint32_t to = map_shared_rank(at, (uint32_t)z);
