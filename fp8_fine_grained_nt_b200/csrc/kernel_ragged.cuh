@@ -38,8 +38,8 @@
 // 1546 TFLOP/s (a library product of that size: 1613); back to back the power
 // limit holds both near 1370.  Few rows per group are bound by reading the
 // weights: 128 rows over 16 groups, N = 4096, K = 7168, 155 us, 6.1 TB/s.
-// Weight gradients of short groups are bound by their epilogue: 1999 rows over
-// 64 groups, 2048 x 520 into BF16, 44 us, 3.3 TB/s.
+// Weight gradients of short groups are bound by writing the result: 1999 rows
+// over 64 groups, 2048 x 520 into BF16, 44 us (a plain fill of those 136 MB: 36).
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN

@@ -29,11 +29,13 @@
 // an adapter's Inf or NaN stays in its rows.  Slots sorted by adapter need one
 // pass almost everywhere.
 //
-// 4096 rows of 8 adapters, rank 64, K = 7168, N = 4096: 45 us, where the bytes
+// 4096 rows of 8 adapters, rank 64, K = 7168, N = 4096: 40 us, where the bytes
 // take 20.5 (clusters of 4 on 128 of the 148 SMs).  The phases follow one
-// another, and none overlaps the next: about 25,000 cycles of reading x, 10,000
-// of exchange (two cluster barriers, reads and writes through distributed shared
-// memory), 23,000 for c, d and the products, the rest set-up.
+// another: 1.6 us until the slots are known, 13.3 of reading x (4.4 TB/s), 6.3
+// of exchange (two cluster barriers, reads and writes through distributed
+// shared memory), 13.2 for c, d and the products (5.1 TB/s), and 4 between the
+// last stores and the next call's start.  x comes by cp.async because TMA picks
+// rows too slowly for 128 bytes of each: 80 cycles for four rows, 65 us in all.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -686,7 +688,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParam
 
 // Long batches with enough slots per adapter; grid.y counts blocks of slots.
 // Measured, short form against this one: 4096 rows of 8 adapters, rank 64, 112
-// against 45 us; 300 rows of one, 24 against 23; 300 rows of 32 (each block of
+// against 40 us; 300 rows of one, 24 against 23; 300 rows of 32 (each block of
 // slots then has a dozen adapters and makes three passes or more) 38 against
 // 150.  Up to 256 slots, at most two clusters, the short form's many CTAs win.
 bool lora_is_wide(int slots, int adapters, int R)
