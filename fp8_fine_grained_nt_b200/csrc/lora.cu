@@ -19,7 +19,7 @@
 // up while the first runs:
 //   down  v in FP32 for a range of k per CTA (`splits` ranges, written side by
 //         side: summed in order by the second kernel, so no atomics)
-//   up    sums the ranges and adds v B^T, in FP32, to c, rounding once.
+//   up    sums the ranges and adds v B^T to c, rounding once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,6 +38,13 @@ constexpr int LORA_THREADS = 256;
 constexpr int LORA_WARPS = 8;
 constexpr int LORA_SLOTS = 16;   // slots per CTA of the first kernel: one MMA's rows
 constexpr int LORA_UP_SLOTS = 8; // of the second
+constexpr int LORA_FP32_RANK = 16; // largest rank whose second product is done in FP32
+
+// bytes of v's sums, or of their shares
+__host__ __device__ constexpr int lora_up_part(int R)
+{
+    return LORA_UP_SLOTS * R > LORA_THREADS * 4 ? LORA_UP_SLOTS * R * 4 : LORA_THREADS * 16;
+}
 
 // 16 x 8 += 16 x 16 * (8 x 16)^T, 16-bit operands, FP32 sums
 template <bool BF16>
@@ -174,7 +181,79 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParam
 
 // ---------------------------------------------------------------- up
 
-// 8 slots and `p.n_chunk` columns per CTA.  A warp's job is 64 columns of one
+// A CTA's slots in the second kernel: segments (runs of one adapter), rows.
+struct UpSlots {
+    float scale[LORA_UP_SLOTS]; // of the slot's adapter
+    int first[LORA_UP_SLOTS + 1], adapter[LORA_UP_SLOTS], row[LORA_UP_SLOTS];
+};
+
+// Segments of 8 slots from slot0 on; returns how many.
+__device__ __forceinline__ int read_segments(const LoraParams &p, int slot0, UpSlots &u, int &adapter)
+{
+    constexpr int SB = LORA_UP_SLOTS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Slot mine = read_slot(p, lane < SB ? slot0 + lane : p.slots);
+    const uint32_t starts = segment_starts(mine.adapter, lane, SB);
+    const int segs = __popc(starts);
+    if (warp == 0 && lane < SB) {
+        if ((starts >> lane) & 1u) {
+            const int i = __popc(starts & ((1u << lane) - 1u));
+            u.first[i] = lane;
+            u.adapter[i] = mine.adapter;
+        }
+        if (lane == 0)
+            u.first[segs] = SB;
+        u.row[lane] = mine.row;
+    }
+    __syncthreads();
+    adapter = mine.adapter;
+    return segs;
+}
+
+// v of the CTA's slots into part[slot][rank / 4] from the first kernel's k
+// ranges.  Thread: one float4 of ranks of one slot, a share of the ranges if
+// there are threads to spare; the shares are joined in order.
+__device__ __forceinline__ void sum_ranges(const LoraParams &p, int slot0, float4 *part)
+{
+    const int tid = threadIdx.x;
+    const int r4 = p.R / 4;
+    const int items = min(LORA_UP_SLOTS, p.slots - slot0) * r4;
+    const int shares = max(1, min(p.splits, LORA_THREADS / items));
+    const int per = (p.splits + shares - 1) / shares;
+    const long step = (long)p.slots * r4;
+    const float4 *src = reinterpret_cast<const float4 *>(p.v) + (long)slot0 * r4;
+    for (int i = tid; i < items * shares; i += LORA_THREADS) {
+        const int item = i % items, z0 = i / items * per, z1 = min(z0 + per, p.splits);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int z = z0; z < z1; ++z) {
+            const float4 v = __ldcg(src + z * step + item);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+        part[i] = sum;
+    }
+    __syncthreads();
+    if (shares > 1) {
+        // (then there are at most LORA_THREADS items, one per thread)
+        if (tid < items) {
+            float4 sum = part[tid];
+            for (int z = 1; z < shares; ++z) {
+                const float4 v = part[z * items + tid];
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            part[tid] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+// Ranks up to 16: 8 slots and `p.n_chunk` columns per CTA.  A warp's job is 64 columns of one
 // segment, two per lane, 16 ranks at a time in FP32: with one or two rows per
 // adapter, as in a decode batch, that takes a third of the instructions of an
 // MMA with its 16 rows (alone, with cold caches, 13.5 -> 8.8 us for 64 rows of
@@ -184,27 +263,14 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
 {
     constexpr int SB = LORA_UP_SLOTS;
     extern __shared__ float4 part[]; // [share][slot][rank / 4]
-    __shared__ float row_scale[SB];
-    __shared__ int seg_first[SB + 1], seg_adapter[SB], slot_row[SB];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ UpSlots u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Everything but v is ready: the first kernel let this one start only
     // after its own wait for the kernels before it.  So the slots and the
     // first job's operands are read while the first kernel runs.
     const int slot0 = blockIdx.x * SB;
-    const Slot mine = read_slot(p, lane < SB ? slot0 + lane : p.slots);
-    const uint32_t starts = segment_starts(mine.adapter, lane, SB);
-    const int segs = __popc(starts);
-    if (warp == 0 && lane < SB) {
-        if ((starts >> lane) & 1u) {
-            const int i = __popc(starts & ((1u << lane) - 1u));
-            seg_first[i] = lane;
-            seg_adapter[i] = mine.adapter;
-        }
-        if (lane == 0)
-            seg_first[segs] = SB;
-        slot_row[lane] = mine.row;
-    }
-    __syncthreads();
+    int adapter;
+    const int segs = read_segments(p, slot0, u, adapter);
 
     const int n_lo = blockIdx.y * p.n_chunk, n_hi = min(n_lo + p.n_chunk, p.N);
     // the job's B: ranks k0 to k0 + 15 of columns n and n + 1 (zero past R; a
@@ -226,7 +292,7 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
         for (int s = 0; s < SB; ++s)
             if (s >= s0 && s < s1 && n < n_hi)
                 cv[s] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.c) +
-                                                            (long)slot_row[s] * p.ld_c + n);
+                                                            (long)u.row[s] * p.ld_c + n);
     };
     int seg = warp - LORA_WARPS, n0 = n_lo;
     auto advance = [&]() { // to this warp's next job
@@ -237,70 +303,32 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
         }
     };
     auto load_job = [&]() {
-        const int g = seg_adapter[seg];
+        const int g = u.adapter[seg];
         if (g >= 0) {
             load_b(g, n0 + 2 * lane, 0);
-            load_c(seg_first[seg], seg_first[seg + 1], n0 + 2 * lane);
+            load_c(u.first[seg], u.first[seg + 1], n0 + 2 * lane);
         }
     };
     advance();
     if (n0 < n_hi)
         load_job();
     if (warp == 0 && lane < SB) // read after the next barriers
-        row_scale[lane] = mine.adapter >= 0 ? __ldg(p.scales + mine.adapter) : 0.0f;
+        u.scale[lane] = adapter >= 0 ? __ldg(p.scales + adapter) : 0.0f;
 
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // v of the CTA's slots.  Thread: one float4 of ranks of one slot, a share
-    // of the k ranges if there are threads to spare; the shares are joined in
-    // order below.
+    sum_ranges(p, slot0, part);
     const int r4 = p.R / 4;
-    const int items = min(SB, p.slots - slot0) * r4;
-    const int shares = max(1, min(p.splits, LORA_THREADS / items));
-    {
-        const int per = (p.splits + shares - 1) / shares;
-        const long step = (long)p.slots * r4;
-        const float4 *src = reinterpret_cast<const float4 *>(p.v) + (long)slot0 * r4;
-        for (int i = tid; i < items * shares; i += LORA_THREADS) {
-            const int item = i % items, z0 = i / items * per, z1 = min(z0 + per, p.splits);
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int z = z0; z < z1; ++z) {
-                const float4 v = __ldcg(src + z * step + item);
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
-            }
-            part[i] = sum;
-        }
-    }
-    __syncthreads();
-    if (shares > 1) {
-        // (then there are at most LORA_THREADS items, one per thread)
-        if (tid < items) {
-            float4 sum = part[tid];
-            for (int z = 1; z < shares; ++z) {
-                const float4 v = part[z * items + tid];
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
-            }
-            part[tid] = sum;
-        }
-        __syncthreads();
-    }
 
     bool loaded = true;
     for (; n0 < n_hi; advance(), loaded = false) {
-        const int g = seg_adapter[seg];
+        const int g = u.adapter[seg];
         if (g < 0)
             continue;
         if (!loaded)
             load_job();
-        const int s0 = seg_first[seg], s1 = seg_first[seg + 1];
+        const int s0 = u.first[seg], s1 = u.first[seg + 1];
         const int n = n0 + 2 * lane;
         float acc[SB][2];
 #pragma unroll
@@ -348,11 +376,148 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
                 if (s < s0 || s >= s1)
                     continue;
                 const float2 old = unpack2<BF16>(cv[s]);
-                const float f = row_scale[s];
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.d) + (long)slot_row[s] * p.ld_d + n) =
+                const float f = u.scale[s];
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.d) + (long)u.row[s] * p.ld_d + n) =
                     pack2<BF16>(fmaf(f, acc[s][0], old.x), fmaf(f, acc[s][1], old.y));
             }
         }
+    }
+}
+
+// Ranks above 16: the same cut, but a warp's job is 32 columns of one segment
+// with mma.sync, v in two 16-bit terms (hi + lo: 16 bits of mantissa with BF16,
+// 22 with FP16, so that the middle result costs no accuracy; an FP16 row is
+// divided by a power of two first, so that v may exceed its range).  Rank 64,
+// 64 rows of 28 adapters, N = 7168, K = 2048: FP32 took 25.6 us a call, most of it reading
+// B, whose columns a lane of that form has 2 R bytes from the next lane's; here
+// four lanes read 64 bytes of a column: 21.5 us (256 rows: 41.5 -> 27.6; rank
+// 32: 17.4 -> 14.4).  The MMA's columns are dealt out so that a lane's results
+// are 8 columns side by side.
+template <bool BF16>
+__global__ void __launch_bounds__(LORA_THREADS, 3) lora_up_mma_kernel(const LoraParams p)
+{
+    constexpr int SB = LORA_UP_SLOTS;
+    extern __shared__ float4 part[]; // [share][slot][rank / 4], then hi and lo [slot][rank]
+    __shared__ UpSlots u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = lane & 3, q = lane >> 2; // q: slot, or column of B
+    // (read early: see above)
+    const int slot0 = blockIdx.x * SB;
+    int adapter;
+    const int segs = read_segments(p, slot0, u, adapter);
+
+    const int n_lo = blockIdx.y * p.n_chunk, n_hi = min(n_lo + p.n_chunk, p.N);
+    int seg = warp - LORA_WARPS, n0 = n_lo;
+    auto advance = [&]() { // to this warp's next job
+        do {
+            seg += LORA_WARPS;
+            while (seg >= segs) {
+                seg -= segs;
+                n0 += 32;
+            }
+        } while (n0 < n_hi && u.adapter[seg] < 0);
+    };
+    // ranks k0 + 8 t to k0 + 8 t + 7 of columns n0 + 8 (q / 2) + q % 2 + 0, 2, 4, 6
+    auto load_b = [&](uint4 (&b)[4], int k0) {
+        const int n = n0 + 8 * (q >> 1) + (q & 1);
+        const bool in = n < n_hi && k0 + 8 * t < p.R; // (N is a multiple of 8)
+        const uint16_t *src = static_cast<const uint16_t *>(p.lora_b) + ((long)u.adapter[seg] * p.N + n) * p.R + k0 + 8 * t;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[j] = in ? __ldg(reinterpret_cast<const uint4 *>(src + 2 * j * (long)p.R)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // columns n0 + 8 t to n0 + 8 t + 7 of slot q
+    auto mine = [&]() { return q >= u.first[seg] && q < u.first[seg + 1] && n0 + 8 * t < n_hi; };
+    auto load_c = [&]() {
+        return mine() ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.c) + (long)u.row[q] * p.ld_c +
+                                                         n0 + 8 * t)
+                      : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 b[4], c = make_uint4(0u, 0u, 0u, 0u);
+    advance();
+    if (n0 < n_hi) {
+        load_b(b, 0);
+        c = load_c();
+    }
+    if (warp == 0 && lane < SB) // read after the next barriers
+        u.scale[lane] = adapter >= 0 ? __ldg(p.scales + adapter) : 0.0f;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    sum_ranges(p, slot0, part);
+
+    // warp: the terms of one slot, with zeros up to a multiple of 32 ranks
+    const int ranks = (p.R + 31) / 32 * 32, pitch = 2 * ranks + 64; // (bytes)
+    const uint32_t hi_at = smem_addr(part) + (uint32_t)lora_up_part(p.R), lo_at = hi_at + (uint32_t)(SB * pitch);
+    {
+        const int r4 = p.R / 4;
+        float amax = 0.0f, power = 1.0f;
+        if constexpr (!BF16) {
+            for (int i = lane; i < r4; i += 32) {
+                const float4 v = part[warp * r4 + i];
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            }
+            power = lora_fp16_scale(amax);
+        }
+        const float inv = 1.0f / power; // a power of two: exact
+        for (int i = lane; i < ranks / 4; i += 32) {
+            const float4 v = i < r4 ? part[warp * r4 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t hi[2], lo[2];
+            split_two<BF16>(v.x * inv, v.y * inv, hi[0], lo[0]);
+            split_two<BF16>(v.z * inv, v.w * inv, hi[1], lo[1]);
+            const uint32_t at = (uint32_t)(warp * pitch + i * 8);
+            st_shared_v2(hi_at + at, hi[0], hi[1]);
+            st_shared_v2(lo_at + at, lo[0], lo[1]);
+        }
+        if (lane == 0)
+            u.scale[warp] *= power;
+    }
+    __syncthreads();
+
+    float acc[4][4] = {};
+    for (int k0 = 0; n0 < n_hi;) {
+        // what comes next is on its way while this is worked on
+        uint16_t *to = static_cast<uint16_t *>(p.d) + (long)u.row[q] * p.ld_d + n0 + 8 * t;
+        const bool store = mine(), last = k0 + 32 >= p.R;
+        const uint32_t at = (uint32_t)(q * pitch + (k0 + 8 * t) * 2);
+        uint4 next_b[4], next_c = c;
+        k0 = last ? 0 : k0 + 32;
+        if (last)
+            advance();
+        if (n0 < n_hi) {
+            load_b(next_b, k0);
+            if (last)
+                next_c = load_c();
+        }
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+            const uint4 v = ld_shared_v4((term ? lo_at : hi_at) + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mma_16816<BF16>(acc[j], v.x, 0u, v.y, 0u, b[j].x, b[j].y);
+                mma_16816<BF16>(acc[j], v.z, 0u, v.w, 0u, b[j].z, b[j].w);
+            }
+        }
+        if (last) {
+            if (store) {
+                const uint32_t old[4] = {c.x, c.y, c.z, c.w};
+                const float f = u.scale[q];
+                uint32_t out[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 o = unpack2<BF16>(old[j]);
+                    out[j] = pack2<BF16>(fmaf(f, acc[j][0], o.x), fmaf(f, acc[j][1], o.y));
+                }
+                st_global_v4(to, out[0], out[1], out[2], out[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[j] = next_b[j];
+        c = next_c;
     }
 }
 
@@ -382,10 +547,12 @@ cudaError_t down(const LoraParams &p, cudaStream_t stream)
 template <bool BF16>
 cudaError_t up(const LoraParams &p, cudaStream_t stream)
 {
-    const size_t sums = sizeof(float) * LORA_UP_SLOTS * p.R, threads = sizeof(float4) * LORA_THREADS;
     const dim3 grid((unsigned)((p.slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS),
                     (unsigned)((p.N + p.n_chunk - 1) / p.n_chunk), 1);
-    return launch_pdl(lora_up_kernel<BF16>, grid, sums > threads ? sums : threads, p, stream);
+    if (p.R <= LORA_FP32_RANK)
+        return launch_pdl(lora_up_kernel<BF16>, grid, (size_t)lora_up_part(p.R), p, stream);
+    const size_t terms = 2u * LORA_UP_SLOTS * (size_t)(2 * ((p.R + 31) / 32 * 32) + 64);
+    return launch_pdl(lora_up_mma_kernel<BF16>, grid, (size_t)lora_up_part(p.R) + terms, p, stream);
 }
 
 template <bool BF16>
@@ -416,7 +583,8 @@ LoraPlan lora_plan(int slots, int R, int N, int K)
     plan.k_chunk = (int)((K + splits * 64 - 1) / (splits * 64) * 64);
     plan.splits = (K + plan.k_chunk - 1) / plan.k_chunk;
     const long up_blocks = slots > 0 ? ((long)slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS : 1;
-    const long chunk = ((long)N * up_blocks + ctas - 1) / ctas;
+    const long up_ctas = (R <= LORA_FP32_RANK ? 4 : 3) * 148;
+    const long chunk = ((long)N * up_blocks + up_ctas - 1) / up_ctas;
     plan.n_chunk = (int)((chunk < N ? chunk : N) + 63) / 64 * 64;
     return plan;
 }

@@ -28,6 +28,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 // v as hi + lo, two 16-bit terms, for two values; an infinite or NaN v has no
 // second one.
 template <bool BF16>
