@@ -687,13 +687,16 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParam
 } // namespace
 
 // Long batches with enough slots per adapter; grid.y counts blocks of slots.
-// Measured, short form against this one: 4096 rows of 8 adapters, rank 64, 112
-// against 40 us; 300 rows of one, 24 against 23; 300 rows of 32 (each block of
-// slots then has a dozen adapters and makes three passes or more) 38 against
-// 150.  Up to 256 slots, at most two clusters, the short form's many CTAs win.
+// Measured, short form against this one, us (N = 4096, K = 7168, rank 64):
+//                     256 rows   512       768       1024      2048
+//   1 adapter         17, 24     21, 24    28, 24    32, 24    55, 35
+//   8 adapters        20, 50     26, 33    32, 31    38, 31    68, 52
+//   8 of rank 16      12, 43     18, 27    22, 26    28, 26    48, 41
+//   32 rows of each   20, 50     28, 51    40, 52    47, 53    102, 88
+// (with fewer rows of each, a block of slots makes more passes)
 bool lora_is_wide(int slots, int adapters, int R)
 {
-    return slots > 256 && R <= 128 && slots / adapters >= 32 && slots <= 65535 * WIDE_SLOTS;
+    return slots > 768 && R <= 128 && slots / adapters >= 32 && slots <= 65535 * WIDE_SLOTS;
 }
 
 int launch_lora_wide(const LoraParams &p, bool bf16, const DeviceView &dev, cudaStream_t stream)

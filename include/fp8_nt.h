@@ -214,8 +214,8 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups);
  * e.g. a dense FP8 GEMM's D, is C).  For slot i with adapter g = m_indices[i]
  * and row t = order[i] (t = i if order is NULL):
  *   D[t,n] = C[t,n] + scales[g] * sum_r ( sum_k X[t,k] A[g,r,k] ) B[g,n,r]
- * with FP32 sums throughout (the inner sums are not rounded to 16 bits) and
- * one rounding to D's type (to nearest even).
+ * with FP32 sums throughout (the inner sums keep at least 16 bits of mantissa:
+ * FP32, or two 16-bit terms) and one rounding to D's type (to nearest even).
  *   X [num_rows] rows of K   A [num_adapters,rank,K]   C, D [num_rows] rows of N
  *   B [num_adapters,N,rank]  scales [num_adapters] FP32
  * all but scales of type dtype (DG_INPUT_BF16 or DG_INPUT_F16).  ld_x, ld_c,

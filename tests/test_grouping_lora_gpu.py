@@ -155,7 +155,7 @@ def sorted_order(ids):
     return sorted((t for t in range(len(ids)) if ids[t] >= 0), key=lambda t: (ids[t], t))
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 64, 256, 257, 300, 700])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 64, 256, 257, 300, 700, 769, 1000])
 @pytest.mark.parametrize("R", [8, 16, 40, 64, 136, 256])
 def test_lora_rows_and_ranks(T, R):
     rng = np.random.default_rng(T * 100 + R)
@@ -165,13 +165,27 @@ def test_lora_rows_and_ranks(T, R):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("N,K", [(8, 8), (8, 2112), (2112, 8), (72, 1032), (4096, 7168)])
-@pytest.mark.parametrize("T", [3, 400])
+@pytest.mark.parametrize("T", [3, 400, 800])
 def test_lora_sizes(dtype, N, K, T):
     ids = [(t // 3) % 4 - 1 for t in range(T)]
     lora_case(T, 3, 16, N, K, dtype, ids, seed=N + K, order=sorted_order(ids))
 
 
-@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("T", [5, 100, 900])
+@pytest.mark.parametrize("R", [24, 64, 128])
+def test_lora_fp16_ranks(T, R):
+    ids = [(t // 7) % 4 - 1 for t in range(T)]
+    lora_case(T, 3, R, 200, 328, FP16, ids, seed=T + R, order=sorted_order(ids))
+
+
+@pytest.mark.parametrize("T", [2100, 4400, 9600])
+@pytest.mark.parametrize("R", [64, 72])
+def test_lora_long_batches(T, R):
+    ids = [t * 5 // T for t in range(T)]
+    lora_case(T, 5, R, 264, 520, BF16, ids, seed=T)
+
+
+@pytest.mark.parametrize("T", [40, 300, 900])
 @pytest.mark.parametrize("kind", ["unsorted", "all_different", "none", "one", "runs"])
 def test_lora_orders(T, kind):
     L = T if kind == "all_different" else 6
@@ -197,9 +211,10 @@ def test_lora_column_ranges_of_wider_tensors():
     assert (wide_d[:, N:] == 7).all()
 
 
-def test_lora_special_values_stay_in_their_rows():
+@pytest.mark.parametrize("R", [16, 40])
+def test_lora_special_values_stay_in_their_rows(R):
     """NaN in a row, Inf in an adapter: other rows of the same 16 are clean."""
-    T, L, R, N, K = 20, 3, 16, 136, 264
+    T, L, N, K = 20, 3, 136, 264
     x, c = gen(T, K, seed=1, dtype=BF16), gen(T, N, seed=2, dtype=BF16)
     A, B = gen(L, R, K, seed=3, dtype=BF16, scale=K ** -0.5), gen(L, N, R, seed=4, dtype=BF16)
     x[3, 5] = float("nan")
@@ -216,15 +231,16 @@ def test_lora_special_values_stay_in_their_rows():
     assert torch.equal(bad, want)
 
 
-def test_lora_special_values_in_long_batches():
+@pytest.mark.parametrize("T", [300, 900])
+def test_lora_special_values_in_long_batches(T):
     """The same where 128 slots of up to three adapters are computed together."""
-    T, L, R, N, K = 300, 3, 16, 136, 264
+    L, R, N, K = 3, 16, 136, 264
     x, c = gen(T, K, seed=1, dtype=BF16), gen(T, N, seed=2, dtype=BF16)
     A, B = gen(L, R, K, seed=3, dtype=BF16, scale=K ** -0.5), gen(L, N, R, seed=4, dtype=BF16)
     x[3, 5] = float("nan")
     A[1, 2, 7] = float("inf")
     B[2, 11, 0] = float("inf")
-    ids = [0] * 100 + [1] * 60 + [2] * 140
+    ids = [0] * 100 + [1] * 60 + [2] * (T - 160)
     d = torch.zeros(T, N, dtype=BF16, device="cuda")
     fp8.m_grouped_lora_add(x, A, B, torch.ones(L, device="cuda"), c, d, torch.tensor(ids, dtype=torch.int32).cuda())
     bad = ~torch.isfinite(d)
@@ -235,9 +251,10 @@ def test_lora_special_values_in_long_batches():
     assert torch.equal(bad, want)
 
 
-def test_lora_fp16_middle_result_beyond_its_range():
+@pytest.mark.parametrize("T,R", [(20, 16), (20, 40), (900, 16), (900, 40)])
+def test_lora_fp16_middle_result_beyond_its_range(T, R):
     """x . A^T is about 2e6, beyond FP16; B brings the result back into it."""
-    T, L, R, N, K = 20, 1, 16, 136, 512
+    L, N, K = 1, 136, 512
     x, A = gen(T, K, seed=1, dtype=FP16, scale=100.0), gen(L, R, K, seed=2, dtype=FP16, scale=1000.0)
     B, c = gen(L, N, R, seed=3, dtype=FP16, scale=1e-3), gen(T, N, seed=4, dtype=FP16)
     d = torch.zeros(T, N, dtype=FP16, device="cuda")
@@ -259,7 +276,7 @@ def test_lora_bad_slots_are_flagged_and_skipped():
         lora_check(d[2:3], x[2:3], A[1], B[1], 1.0, c[2:3])
 
 
-@pytest.mark.parametrize("T", [5, 400])
+@pytest.mark.parametrize("T", [5, 400, 900])
 def test_lora_negative_slots(T):
     x, A, B = gen(T, 64, seed=1, dtype=BF16), gen(2, 8, 64, seed=2, dtype=BF16), gen(2, 64, 8, seed=3, dtype=BF16)
     scale, c = torch.ones(2, device="cuda"), gen(T, 64, seed=4, dtype=BF16)
