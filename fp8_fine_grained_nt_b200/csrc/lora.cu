@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParam
     const uint32_t starts = segment_starts(mine.adapter, lane, SB);
     const int segs = __popc(starts);
     const int slices = max(1, LORA_WARPS / segs);
-    const int k_lo = blockIdx.z * p.k_chunk, k_hi = min(k_lo + p.k_chunk, p.K);
+    // (the end of a range is taken from what is left: K and N may be near 2^31)
+    const int k_lo = blockIdx.z * p.k_chunk, k_hi = k_lo + min(p.k_chunk, p.K - k_lo);
     const int k_step = ((k_hi - k_lo + slices - 1) / slices + 31) / 32 * 32;
 
     for (int job = warp; job < segs * slices; job += LORA_WARPS) {
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
     int adapter;
     const int segs = read_segments(p, slot0, u, adapter);
 
-    const int n_lo = blockIdx.y * p.n_chunk, n_hi = min(n_lo + p.n_chunk, p.N);
+    const int n_lo = blockIdx.y * p.n_chunk, n_hi = n_lo + min(p.n_chunk, p.N - n_lo);
     // the job's B: ranks k0 to k0 + 15 of columns n and n + 1 (zero past R; a
     // column pair past the end reads the last one's and is not stored)
     uint4 b[2][2];
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(LORA_THREADS, 3) lora_up_mma_kernel(const Lora
     int adapter;
     const int segs = read_segments(p, slot0, u, adapter);
 
-    const int n_lo = blockIdx.y * p.n_chunk, n_hi = min(n_lo + p.n_chunk, p.N);
+    const int n_lo = blockIdx.y * p.n_chunk, n_hi = n_lo + min(p.n_chunk, p.N - n_lo);
     int seg = warp - LORA_WARPS, n0 = n_lo;
     auto advance = [&]() { // to this warp's next job
         do {
@@ -550,7 +551,7 @@ template <bool BF16>
 cudaError_t up(const LoraParams &p, cudaStream_t stream)
 {
     const dim3 grid((unsigned)((p.slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS),
-                    (unsigned)((p.N + p.n_chunk - 1) / p.n_chunk), 1);
+                    (unsigned)(((long)p.N + p.n_chunk - 1) / p.n_chunk), 1);
     if (p.R <= LORA_FP32_RANK)
         return launch_pdl(lora_up_kernel<BF16>, grid, (size_t)lora_up_part(p.R), p, stream);
     const size_t terms = 2u * LORA_UP_SLOTS * (size_t)(2 * ((p.R + 31) / 32 * 32) + 64);
@@ -584,7 +585,7 @@ LoraPlan lora_plan(int slots, int R, int N, int K)
     const long most = (K + 63) / 64 < 32 ? (K + 63) / 64 : 32;
     splits = splits < 1 ? 1 : splits > most ? most : splits;
     plan.k_chunk = (int)((K + splits * 64 - 1) / (splits * 64) * 64);
-    plan.splits = (K + plan.k_chunk - 1) / plan.k_chunk;
+    plan.splits = (int)(((long)K + plan.k_chunk - 1) / plan.k_chunk);
     const long up_blocks = slots > 0 ? ((long)slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS : 1;
     const long up_ctas = (R <= LORA_FP32_RANK ? 4 : 3) * 148;
     const long chunk = ((long)N * up_blocks + up_ctas - 1) / up_ctas;

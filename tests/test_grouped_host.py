@@ -110,6 +110,17 @@ def test_lora_columns_near_2_to_31(lib):
     assert lib.get_lora_workspace_size(1, 1, 8, 0x7fff0000, 64) > 0
 
 
+@pytest.mark.parametrize("slots", [1, 24, 512, 768])
+@pytest.mark.parametrize("rank", [8, 64, 256])
+def test_lora_workspace_near_2_to_31(lib, slots, rank):
+    """The largest N and K are cut into ranges like any other: between one and
+    32 ranges of k, FP32 sums of each."""
+    for N, K in ((64, 0x7fff0000), (0x7fff0000, 64), (64, 2080000000), (64, 0x7fff0000 - 8)):
+        size = lib.get_lora_workspace_size(slots, 1000, rank, N, K)
+        splits = size // (slots * rank * 4)
+        assert size == splits * slots * rank * 4 and 1 <= splits <= 32
+
+
 def test_force_ragged(lib):
     try:
         for form in ((1, 0, 16, 8), (1, 0, 64, 4), (1, 0, 16), (1, 0, 32), (1, 0, 64), (1, 0, 128), (0, 1, 256), (0, 0, 256), (0, 0, 128), (0, 0, 0)):
