@@ -43,7 +43,7 @@
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
-// only), warps 4-11 epilogue (a 32-lane quarter of tensor memory and half of the
+// only), warp 3 hands back received sums (shared reductions), warps 4-11 epilogue (a 32-lane quarter of tensor memory and half of the
 // tile's columns each).  Two accumulators in tensor memory let a tile's
 // epilogue overlap the next tile's MMAs.
 #pragma once
@@ -166,12 +166,13 @@ __device__ __forceinline__ void drain_ragged(uint64_t *bar, uint32_t parity, vol
 }
 
 // The same for a barrier that other CTAs of the cluster arrive on after writing
-// this one's shared memory.
+// this one's shared memory, or after reading what this one is to write again.
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag,
                                              const RaggedParams &p)
 {
+    // (a fence would also wait for this thread's own stores on their way)
     const bool got = wait_ragged(bar, parity, abort_flag, p);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    mbar_acquire_cluster(smem_addr(bar), parity);
     return got;
 }
 
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     uint64_t *mma_done = acc_empty + 2;
     uint64_t *recv_full = mma_done + 1; // split: every CTA's sums for this one's token rows are here
     uint64_t *recv_free = recv_full + 1; // split: every CTA has read what this one sent
+    uint64_t *recv_read = recv_free + 1; // split: this CTA's epilogue has read what it received
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + p.off_misc);
     volatile uint32_t *abort_flag = misc + 1;
     int *tiles = reinterpret_cast<int *>(smem + p.off_groups);
@@ -254,7 +256,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
         }
         mbar_init(mma_done, 1);
         mbar_init(recv_full, 4u * (uint32_t)p.split);
-        mbar_init(recv_free, 8u * (uint32_t)p.split);
+        mbar_init(recv_free, (uint32_t)p.split);
+        mbar_init(recv_read, 8);
         misc[1] = 0u;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmap_x);
@@ -449,8 +452,10 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     if constexpr (TN) {
                         // a segment's last block is announced by warp 2
                         const bool tail = ti.rows - kb * T::BK < T::BK;
-                        if (!wait_ragged(tail ? &tail_ready[s] : &full[s],
-                                         ((tail ? tail_phase : full_phase) >> s) & 1, abort_flag, p)) {
+                        const uint32_t parity = ((tail ? tail_phase : full_phase) >> s) & 1;
+                        // (a pair's is announced by both CTAs, each after writes to its own memory)
+                        if (!(PAIR && tail ? wait_cluster(&tail_ready[s], parity, abort_flag, p)
+                                           : wait_ragged(tail ? &tail_ready[s] : &full[s], parity, abort_flag, p))) {
                             ok = false;
                             break;
                         }
@@ -545,6 +550,21 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
     } else if (warp == 3) {
         if constexpr (F32)
             regs_dec<RAGGED_REGS_OTHER>();
+        // ------------------------------------------------------------ hand-back of received sums (split)
+        // The other CTAs' next writes come after this one's reads: a release at
+        // cluster scope, by a warp that has no stores on their way.  From the
+        // epilogue warps it would wait for those of the tile before (64 groups of
+        // 8 rows, N = 2112, K = 2048, shared by 8: 235 -> 294 us).
+        if (split) {
+            uint32_t parity = 0;
+            for (int t = t_first; t < num_tiles; t += t_stride, parity ^= 1u) {
+                const bool got = wait_ragged(recv_read, parity, abort_flag, p);
+                if (!__all_sync(0xffffffffu, got))
+                    break;
+                if (lane < p.split)
+                    mbar_arrive_cluster_release(map_shared_rank(smem_addr(recv_free), (uint32_t)lane));
+            }
+        }
     } else {
         // ------------------------------------------------------------ epilogue
         if constexpr (F32) // these warps hold the sums
@@ -659,7 +679,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     if (lane == 0)
                         mbar_arrive(&acc_empty[buf]);
                     // what was sent for the tile before has been read everywhere
-                    bool got = wait_ragged(recv_free, (tile_it & 1) ^ 1, abort_flag, p);
+                    bool got = wait_cluster(recv_free, (tile_it & 1) ^ 1, abort_flag, p);
                     if (!__all_sync(0xffffffffu, got))
                         break;
                     // received: [source][owned token row][128 columns]
@@ -682,8 +702,7 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                     if (!__all_sync(0xffffffffu, got))
                         break;
                     // the owned token rows: 256 threads, a column each, every other
-                    // row.  The buffer is handed back before the stores: a
-                    // release would wait for them.
+                    // row.  Warp 3 hands the buffer back.
                     const int x = (int)threadIdx.x - 128;
                     const int col = ti.i0 + (x & 127);
                     float sum[BN / 4];
@@ -696,8 +715,8 @@ __global__ void __launch_bounds__(RAGGED_THREADS, 1)
                                 sum[i] += ld_shared_f32(recv + (uint32_t)(((z * own + t0) * 128 + (x & 127)) * 4));
                     }
                     __syncwarp();
-                    if (lane < p.split)
-                        mbar_arrive_cluster(map_shared_rank(smem_addr(recv_free), (uint32_t)lane));
+                    if (lane == 0)
+                        mbar_arrive(recv_read);
 #pragma unroll
                     for (int i = 0; i < BN / 4; ++i) {
                         const int t0 = (x >> 7) + 2 * i, tok = (int)rank * own + t0;

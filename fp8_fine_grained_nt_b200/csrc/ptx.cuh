@@ -59,6 +59,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
     return done != 0;
 }
 
+// The same test at cluster scope, for a phase that has completed: what other
+// CTAs of the cluster released before their arrivals is ordered before what
+// follows.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar_addr, uint32_t parity)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar_addr),
+        "r"(parity)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- launch order
 
 // Wait until the grids this one depends on (programmatic dependent launch)
@@ -587,7 +599,7 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t x_desc, uint64
 }
 
 // Arrive on a barrier of another CTA of the cluster, releasing this thread's
-// earlier shared-memory writes to it.
+// earlier shared-memory accesses to it.
 __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar_cluster)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");

@@ -88,7 +88,7 @@ inline void make_ragged_plan(RaggedParams &p, uint32_t stage_bytes, int stages, 
     p.off_recv = p.off_out + 8u * (uint32_t)out_slots * RAGGED_SLOT_BYTES;
     p.off_groups = p.off_recv + recv_bytes;
     p.off_bars = align_up_u32(p.off_groups + 4u * (3u * (uint32_t)p.num_groups + 1u), 8);
-    p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 7u), 16);
+    p.off_misc = align_up_u32(p.off_bars + 8u * (4u * RAGGED_MAX_STAGES + 8u), 16);
     p.total = p.off_misc + 80;
 }
 
