@@ -914,6 +914,7 @@ int current_device(DeviceView *out)
         return st;
     out->index = (int)(dev - g_devices);
     out->sms = effective_sms(dev);
+    out->bounded = out->sms < dev->sm_count;
     out->max_smem = dev->max_smem;
     out->status = dev->status;
     out->timeout_ns = wait_timeout_ns();

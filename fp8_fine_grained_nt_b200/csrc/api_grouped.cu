@@ -36,15 +36,6 @@ long ceil_div(long a, long b) { return (a + b - 1) / b; }
 constexpr int kMaxSize = 0x7fff0000; // rows of a product, N and K: 32-bit coordinates, with room for the last tile
 constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, with room to round up
 
-// Clusters of `together` CTAs, one CTA per SM, that run at once on `sms` SMs:
-// clusters of 4 and 8 do not fill the GPCs of a 148-SM part (measured: 33, 15).
-int clusters_held(int together, int sms)
-{
-    const int most = together == 4 ? 33 : together == 8 ? 15 : 148 / together;
-    const int n = sms / together < most ? sms / together : most;
-    return n > 0 ? n : 1;
-}
-
 // Time of a call in us by a wave model of the tile forms, with the mean rows per
 // group (the host does not know more) and counts spread evenly from none to
 // twice the mean.  Back to back, these calls run under the power limit (1.2 to
@@ -354,7 +345,7 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups)
         return -DG_ERR_INVALID_ARGUMENT;
     if (num_groups > RAGGED_MAX_GROUPS || num_rows > kMaxSlots)
         return -DG_ERR_UNSUPPORTED_SHAPE;
-    const long chunks = ceil_div(num_rows, group_rows_chunk(num_rows));
+    const long chunks = ceil_div(num_rows, group_rows_chunk(num_rows, GROUP_MAX_CHUNKS));
     return chunks > 1 ? (long long)chunks * num_groups * 4 : 0;
 }
 
@@ -381,7 +372,7 @@ int group_rows_by_index(const void *index, int index_dtype, int *offsets, int *o
     if (st != DG_OK)
         return st;
     return launch_group_rows(index, index_dtype == DG_INDEX_I64, num_rows, num_groups, alignment, capacity, offsets,
-                             order, slots, m_indices, static_cast<int *>(workspace), dev.status, dev.index,
+                             order, slots, m_indices, static_cast<int *>(workspace), dev,
                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DG_OK
                : DG_ERR_CUDA;
@@ -396,7 +387,7 @@ long long get_lora_workspace_size(int num_slots, int num_adapters, int rank, int
         return -DG_ERR_UNSUPPORTED_SHAPE;
     if (num_slots == 0 || lora_is_wide(num_slots, num_adapters, rank))
         return 0;
-    return (long long)lora_plan(num_slots, rank, N, K).splits * num_slots * rank * 4;
+    return lora_workspace(num_slots, rank, N, K);
 }
 
 int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const void *lora_b, const float *scales,
@@ -448,11 +439,7 @@ int m_grouped_lora_add(const void *x, long long ld_x, const void *lora_a, const 
     p.K = K;
     if (lora_is_wide(num_slots, num_adapters, rank))
         return launch_lora_wide(p, dtype == DG_INPUT_BF16, dev, reinterpret_cast<cudaStream_t>(stream));
-    const LoraPlan plan = lora_plan(num_slots, rank, N, K);
-    p.k_chunk = plan.k_chunk;
-    p.splits = plan.splits;
-    p.n_chunk = plan.n_chunk;
-    return launch_lora(p, dtype == DG_INPUT_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_lora(p, dtype == DG_INPUT_BF16, dev, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DG_OK
                : DG_ERR_CUDA;
 }

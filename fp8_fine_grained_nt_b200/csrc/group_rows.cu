@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) group_place_kernel(const GroupA
 }
 
 template <bool I64>
-cudaError_t launch(const GroupArgs &a, int device, cudaStream_t stream)
+cudaError_t launch(const GroupArgs &a, int device, bool bounded, cudaStream_t stream)
 {
     const size_t count_smem = sizeof(int) * (size_t)GROUP_WARPS * a.groups;
     const size_t place_smem = count_smem + sizeof(int) * (2u * (size_t)a.groups + 1u);
@@ -283,7 +283,7 @@ cudaError_t launch(const GroupArgs &a, int device, cudaStream_t stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = bounded ? 0 : 1; // (two kernels at once would take twice the SMs of one)
     if (a.chunks > 1) {
         const cudaError_t err = cudaLaunchKernelEx(&cfg, group_count_kernel<I64>, a);
         if (err != cudaSuccess)
@@ -296,12 +296,12 @@ cudaError_t launch(const GroupArgs &a, int device, cudaStream_t stream)
 } // namespace
 
 // Rows per chunk, a multiple of GROUP_THREADS: up to 2048 rows in one chunk
-// (one launch), else chunks of 2048, growing so that at most 256 chunks'
-// counts are added up by every CTA.
-int group_rows_chunk(int rows)
+// (one launch), else chunks of 2048, growing so that every CTA adds up the
+// counts of at most GROUP_MAX_CHUNKS chunks, or of as many as there may be CTAs.
+int group_rows_chunk(int rows, int max_chunks)
 {
-    const int most = 256, unit = 4 * GROUP_THREADS;
-    int chunk = rows <= unit ? rows : (rows + most - 1) / most;
+    const int unit = 4 * GROUP_THREADS;
+    int chunk = rows <= unit ? rows : (int)(((long)rows + max_chunks - 1) / max_chunks);
     if (rows > unit && chunk < unit)
         chunk = unit;
     chunk = (chunk + GROUP_THREADS - 1) / GROUP_THREADS * GROUP_THREADS;
@@ -309,8 +309,8 @@ int group_rows_chunk(int rows)
 }
 
 cudaError_t launch_group_rows(const void *index, bool i64, int rows, int groups, int alignment, int capacity,
-                              int *offsets, int *order, int *slots, int *m_indices, int *counts, unsigned int *status,
-                              int device, cudaStream_t stream)
+                              int *offsets, int *order, int *slots, int *m_indices, int *counts,
+                              const DeviceView &dev, cudaStream_t stream)
 {
     GroupArgs a;
     a.index = index;
@@ -319,14 +319,14 @@ cudaError_t launch_group_rows(const void *index, bool i64, int rows, int groups,
     a.slots = slots;
     a.m_indices = m_indices;
     a.counts = counts;
-    a.status = status;
+    a.status = dev.status;
     a.rows = rows;
     a.groups = groups;
     a.alignment = alignment;
     a.capacity = capacity;
-    a.chunk = group_rows_chunk(rows);
+    a.chunk = group_rows_chunk(rows, dev.bounded && dev.sms < GROUP_MAX_CHUNKS ? dev.sms : GROUP_MAX_CHUNKS);
     a.chunks = rows > 0 ? (rows + a.chunk - 1) / a.chunk : 1;
-    return i64 ? launch<true>(a, device, stream) : launch<false>(a, device, stream);
+    return i64 ? launch<true>(a, dev.index, dev.bounded, stream) : launch<false>(a, dev.index, dev.bounded, stream);
 }
 
 } // namespace fp8nt

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_down_kernel(const LoraParam
     grid_dependency_wait();
     grid_launch_dependents();
     const int slot0 = blockIdx.x * SB;
-    const int r0 = blockIdx.y * RB;
+    const int r0 = (blockIdx.y + p.rank_block) * RB;
     const Slot mine = read_slot(p, lane < SB ? slot0 + lane : p.slots);
     const uint32_t starts = segment_starts(mine.adapter, lane, SB);
     const int segs = __popc(starts);
@@ -524,7 +524,10 @@ __global__ void __launch_bounds__(LORA_THREADS, 3) lora_up_mma_kernel(const Lora
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(LoraParams), dim3 grid, size_t smem, const LoraParams &p, cudaStream_t stream)
+// Overlapping the kernel before (`overlap`), except under a bound on the SMs,
+// where two kernels at once would take more.
+cudaError_t launch_one(void (*kernel)(LoraParams), dim3 grid, size_t smem, const LoraParams &p, bool overlap,
+                       cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -535,67 +538,119 @@ cudaError_t launch_pdl(void (*kernel)(LoraParams), dim3 grid, size_t smem, const
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = overlap ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <bool BF16, int NT>
-cudaError_t down(const LoraParams &p, cudaStream_t stream)
+cudaError_t down(LoraParams p, bool overlap, int most_rank_blocks, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((p.slots + LORA_SLOTS - 1) / LORA_SLOTS), (unsigned)((p.R + 8 * NT - 1) / (8 * NT)),
-                    (unsigned)p.splits);
-    return launch_pdl(lora_down_kernel<BF16, NT>, grid, 0, p, stream);
+    const int rank_blocks = (p.R + 8 * NT - 1) / (8 * NT);
+    cudaError_t err = cudaSuccess;
+    for (p.rank_block = 0; err == cudaSuccess && p.rank_block < rank_blocks; p.rank_block += most_rank_blocks) {
+        const int n = min(most_rank_blocks, rank_blocks - p.rank_block);
+        const dim3 grid((unsigned)((p.slots + LORA_SLOTS - 1) / LORA_SLOTS), (unsigned)n, (unsigned)p.splits);
+        err = launch_one(lora_down_kernel<BF16, NT>, grid, 0, p, overlap, stream);
+    }
+    return err;
 }
 
 template <bool BF16>
-cudaError_t up(const LoraParams &p, cudaStream_t stream)
+cudaError_t up(const LoraParams &p, bool overlap, cudaStream_t stream)
 {
     const dim3 grid((unsigned)((p.slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS),
                     (unsigned)(((long)p.N + p.n_chunk - 1) / p.n_chunk), 1);
     if (p.R <= LORA_FP32_RANK)
-        return launch_pdl(lora_up_kernel<BF16>, grid, (size_t)lora_up_part(p.R), p, stream);
+        return launch_one(lora_up_kernel<BF16>, grid, (size_t)lora_up_part(p.R), p, overlap, stream);
     const size_t terms = 2u * LORA_UP_SLOTS * (size_t)(2 * ((p.R + 31) / 32 * 32) + 64);
-    return launch_pdl(lora_up_mma_kernel<BF16>, grid, (size_t)lora_up_part(p.R) + terms, p, stream);
+    return launch_one(lora_up_mma_kernel<BF16>, grid, (size_t)lora_up_part(p.R) + terms, p, overlap, stream);
 }
 
 template <bool BF16>
-cudaError_t both(const LoraParams &p, cudaStream_t stream)
+cudaError_t both(const LoraParams &p, bool overlap, int most_rank_blocks, cudaStream_t stream)
 {
-    const cudaError_t err = p.R <= 16 ? down<BF16, 2>(p, stream)
-                          : p.R <= 32 ? down<BF16, 4>(p, stream) : down<BF16, 8>(p, stream);
+    const cudaError_t err = p.R <= 16 ? down<BF16, 2>(p, overlap, most_rank_blocks, stream)
+                          : p.R <= 32 ? down<BF16, 4>(p, overlap, most_rank_blocks, stream)
+                                      : down<BF16, 8>(p, overlap, most_rank_blocks, stream);
     if (err != cudaSuccess)
         return err;
-    return up<BF16>(p, stream);
+    return up<BF16>(p, overlap, stream);
 }
 
-} // namespace
+long slot_blocks(int slots, int size) { return slots > 0 ? ((long)slots + size - 1) / size : 1; }
+
+// k in `splits` ranges, or a few less: multiples of 64, at least that.
+void set_splits(LoraParams &p, long splits)
+{
+    const long most = min(((long)p.K + 63) / 64, 32L);
+    splits = splits < 1 ? 1 : splits > most ? most : splits;
+    p.k_chunk = (int)((p.K + splits * 64 - 1) / (splits * 64) * 64);
+    p.splits = (int)(((long)p.K + p.k_chunk - 1) / p.k_chunk);
+}
+
+// N in `chunks` chunks, or a few less.
+void set_columns(LoraParams &p, long chunks)
+{
+    const long chunk = ((long)p.N + chunks - 1) / chunks;
+    p.n_chunk = (int)((chunk + 63) / 64 * 64);
+}
 
 // How a call is cut up, from its sizes alone (the workspace follows from it):
 // k ranges and column chunks so that either kernel has about four CTAs per SM
 // (three with mma.sync in the second: rank 64, 64 rows 21.5 us, 24.6 with four),
 // at most 32 ranges (which the second kernel adds up in one or two rounds of
 // loads), at least 64 wide.
-LoraPlan lora_plan(int slots, int R, int N, int K)
+void lora_plan(LoraParams &p)
 {
-    LoraPlan plan = {};
-    const long ctas = 4 * 148;
-    const long blocks = slots > 0 ? ((long)slots + LORA_SLOTS - 1) / LORA_SLOTS : 1;
-    const long down_blocks = blocks * ((R + 63) / 64);
-    long splits = ctas / down_blocks;
-    const long most = (K + 63) / 64 < 32 ? (K + 63) / 64 : 32;
-    splits = splits < 1 ? 1 : splits > most ? most : splits;
-    plan.k_chunk = (int)((K + splits * 64 - 1) / (splits * 64) * 64);
-    plan.splits = (int)(((long)K + plan.k_chunk - 1) / plan.k_chunk);
-    const long up_blocks = slots > 0 ? ((long)slots + LORA_UP_SLOTS - 1) / LORA_UP_SLOTS : 1;
-    const long up_ctas = (R <= LORA_FP32_RANK ? 4 : 3) * 148;
-    const long chunk = ((long)N * up_blocks + up_ctas - 1) / up_ctas;
-    plan.n_chunk = (int)((chunk < N ? chunk : N) + 63) / 64 * 64;
-    return plan;
+    set_splits(p, 4 * 148 / (slot_blocks(p.slots, LORA_SLOTS) * ((p.R + 63) / 64)));
+    const long up_ctas = (p.R <= LORA_FP32_RANK ? 4 : 3) * 148;
+    const long chunk = ((long)p.N * slot_blocks(p.slots, LORA_UP_SLOTS) + up_ctas - 1) / up_ctas;
+    p.n_chunk = (int)((min(chunk, (long)p.N) + 63) / 64 * 64);
 }
 
-cudaError_t launch_lora(const LoraParams &p, bool bf16, cudaStream_t stream)
+// Under a bound on the SMs no launch has more CTAs than that: as many slots at a
+// time as go into it, k and N cut so that the rest of the SMs have work too.
+template <bool BF16>
+cudaError_t launch_bounded(const LoraParams &all, int sms, cudaStream_t stream)
 {
-    return bf16 ? both<true>(p, stream) : both<false>(p, stream);
+    const int rank_blocks = all.R <= 32 ? 1 : (all.R + 63) / 64;
+    const int wide = rank_blocks > 2 ? rank_blocks : 2; // most CTAs of either kernel per block of 16 slots
+    const int blocks = (int)min(slot_blocks(all.slots, LORA_SLOTS), (long)(sms / wide > 0 ? sms / wide : 1));
+    const int step = sms > 1 ? blocks * LORA_SLOTS : LORA_UP_SLOTS;
+    for (int first = 0; first < all.slots; first += step) {
+        LoraParams p = lora_piece(all, first, min(step, all.slots - first));
+        // (within the workspace of the call, which the pieces use in turn)
+        const long room = (long)all.splits * all.slots / p.slots;
+        set_splits(p, min((long)(sms / (blocks * rank_blocks)), room));
+        set_columns(p, max(1L, sms / slot_blocks(p.slots, LORA_UP_SLOTS)));
+        const cudaError_t err = both<BF16>(p, false, min(rank_blocks, sms), stream);
+        if (err != cudaSuccess)
+            return err;
+    }
+    return cudaSuccess;
+}
+
+} // namespace
+
+long long lora_workspace(int slots, int R, int N, int K)
+{
+    LoraParams p = {};
+    p.slots = slots;
+    p.R = R;
+    p.N = N;
+    p.K = K;
+    lora_plan(p);
+    return (long long)p.splits * slots * R * 4;
+}
+
+cudaError_t launch_lora(const LoraParams &call, bool bf16, const DeviceView &dev, cudaStream_t stream)
+{
+    LoraParams p = call;
+    lora_plan(p);
+    if (dev.bounded)
+        return bf16 ? launch_bounded<true>(p, dev.sms, stream) : launch_bounded<false>(p, dev.sms, stream);
+    const int all = LORA_MAX_RANK; // blocks of ranks
+    return bf16 ? both<true>(p, true, all, stream) : both<false>(p, true, all, stream);
 }
 
 } // namespace fp8nt

@@ -625,13 +625,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 }
 
 // Shared memory of a call: see the kernel's phases.
-WidePlan wide_plan(int slots, int R)
+WidePlan wide_plan(int slots, int R, int sms)
 {
     WidePlan w = {};
     const int blocks = (slots + WIDE_SLOTS - 1) / WIDE_SLOTS;
-    // as many CTAs per block of slots as run at once (clusters of 8, 4 and 2
-    // with one CTA per SM that a 148-SM part holds: 15, 33 and 74)
-    w.cluster = blocks <= 15 ? 8 : blocks <= 33 ? 4 : blocks <= 74 ? 2 : 1;
+    // as many CTAs per block of slots as run at once
+    w.cluster = 8;
+    while (w.cluster > 1 && (w.cluster > sms || blocks > clusters_held(w.cluster, sms)))
+        w.cluster /= 2;
     const uint32_t chunks = (uint32_t)(R + 63) / 64;
     w.segs = R <= 64 ? 4 : 1;
     w.a_bytes = (uint32_t)(R + 15) / 16 * 16 * 128;
@@ -657,6 +658,18 @@ template <bool BF16>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParams &wp, const DeviceView &dev,
                    cudaStream_t stream)
 {
+    // under a bound on the SMs, as many blocks of slots at a time as go into it
+    // (and no overlap of the launches)
+    const int most = clusters_held(wp.plan.cluster, dev.sms) * WIDE_SLOTS;
+    if (dev.bounded && wp.p.slots > most) {
+        cudaError_t err = cudaSuccess;
+        for (int first = 0; err == cudaSuccess && first < wp.p.slots; first += most) {
+            WideParams piece = wp;
+            piece.p = lora_piece(wp.p, first, min(most, wp.p.slots - first));
+            err = launch<BF16>(ta, tb, piece, dev, stream);
+        }
+        return err;
+    }
     static std::atomic<bool> ready[64];
     auto kernel = lora_wide_kernel<BF16>;
     const int smem = (int)wp.plan.total + 1024;
@@ -673,14 +686,14 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParam
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)wp.plan.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)wp.plan.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = dev.bounded ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kernel, ta, tb, wp);
 }
 
@@ -704,7 +717,7 @@ int launch_lora_wide(const LoraParams &p, bool bf16, const DeviceView &dev, cuda
     WideParams wp;
     memset(&wp, 0, sizeof(wp));
     wp.p = p;
-    wp.plan = wide_plan(p.slots, p.R);
+    wp.plan = wide_plan(p.slots, p.R, dev.sms);
     if ((int)wp.plan.total + 1024 > dev.max_smem - 4096)
         return DG_ERR_UNSUPPORTED_SHAPE;
     const int ranks = (p.R + 15) / 16 * 16;
