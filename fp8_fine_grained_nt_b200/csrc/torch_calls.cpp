@@ -12,6 +12,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fp8_nt.h"
@@ -191,15 +192,14 @@ long long lora_add(PyObject *const *args)
 template <long long (*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
+    // (C++ exceptions become torch's own in Python: no memory for the workspace is
+    // its OutOfMemoryError, as from binding.py)
+    HANDLE_TH_ERRORS
     if (n != N)
         return PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
-    try {
-        const long long status = F(args);
-        return PyErr_Occurred() ? nullptr : PyLong_FromLongLong(status); // (an argument's own error)
-    } catch (const std::exception &e) { // e.g. no memory for the workspace
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    const long long status = F(args);
+    return PyErr_Occurred() ? nullptr : PyLong_FromLongLong(status); // (an argument's own error)
+    END_HANDLE_TH_ERRORS
 }
 
 #define FP8NT_ENTRY(name, f, n)                                                                                       \

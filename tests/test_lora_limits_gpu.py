@@ -32,6 +32,30 @@ def test_columns_near_2_to_31(slots):
     assert not d[0, T:N - T].any()
 
 
+@pytest.mark.parametrize("named_stream", [False, True])
+def test_no_memory_for_the_workspace(named_stream):
+    """torch's own error whichever way the call goes, and the next call works."""
+    T, L, R, N, K = 40960, 4, 256, 8, 64
+    need = fp8.get_lora_workspace_size(T, L, R, N, K)
+    assert need > 32 << 20   # a block of its own, not a part of one that is there
+    x, A = gen(T, K, seed=1, dtype=BF16), gen(L, R, K, seed=2, dtype=BF16, scale=K ** -0.5)
+    B, c = gen(L, N, R, seed=3, dtype=BF16), gen(T, N, seed=4, dtype=BF16)
+    ids, d = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, N, dtype=BF16, device="cuda")
+    args = (x, A, B, torch.ones(L, device="cuda"), c, d, ids)
+    stream = dict(stream=torch.cuda.current_stream()) if named_stream else {}
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            fp8.m_grouped_lora_add(*args, **stream)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not d.any()
+    fp8.m_grouped_lora_add(*args, **stream)
+    lora_check(d, x, A[0], B[0], 1.0, c)
+
+
 def test_long_sums_near_2_to_31():
     """The last of the ranges of k ends near 2^31 (A: 34 GB, zero but for both ends)."""
     R, N, K, T = 8, 64, MOST, 2048
