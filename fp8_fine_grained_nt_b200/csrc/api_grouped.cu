@@ -197,7 +197,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     const int red = dir == RAGGED_NT ? K : N; // reduction of NT, NN
     p.d_rows = N;
     p.d_cols = out;
-    const int halves = ragged_halves(k->swap, k->pair, k->bn);
+    const int halves = ragged_halves(k->swap, k->pair);
     p.nkb = (int)ceil_div(red, 64 * halves);
     long tiles;
     if (tn) {

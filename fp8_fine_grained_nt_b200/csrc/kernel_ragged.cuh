@@ -69,7 +69,7 @@ struct RaggedTraits {
     static constexpr uint32_t HALF_BYTES = X_BYTES + Y_BYTES;
     // 64-wide blocks of the reduction per stage: with two, one wait and one
     // commit serve eight MMAs
-    static constexpr int H = ragged_halves(SWAP, PAIR, BN);
+    static constexpr int H = ragged_halves(SWAP, PAIR);
     static constexpr int BK = 64 * H;
     static constexpr uint32_t STAGE_BYTES = H * HALF_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;

@@ -257,7 +257,7 @@ __device__ __forceinline__ void sum_ranges(const LoraParams &p, int slot0, float
 }
 
 // Ranks up to 16: 8 slots and `p.n_chunk` columns per CTA.  A warp's job is 64 columns of one
-// segment, two per lane, 16 ranks at a time in FP32: with one or two rows per
+// segment, two per lane, all ranks in FP32: with one or two rows per
 // adapter, as in a decode batch, that takes a third of the instructions of an
 // MMA with its 16 rows (alone, with cold caches, 13.5 -> 8.8 us for 64 rows of
 // 28 adapters, N = 7168).
@@ -276,18 +276,17 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
     const int segs = read_segments(p, slot0, u, adapter);
 
     const int n_lo = blockIdx.y * p.n_chunk, n_hi = n_lo + min(p.n_chunk, p.N - n_lo);
-    // the job's B: ranks k0 to k0 + 15 of columns n and n + 1 (zero past R; a
+    // the job's B: the 8 or 16 ranks of columns n and n + 1 (zero past R; a
     // column pair past the end reads the last one's and is not stored)
     uint4 b[2][2];
-    auto load_b = [&](int g, int n, int k0) {
-        const uint16_t *base =
-            static_cast<const uint16_t *>(p.lora_b) + ((long)g * p.N + min(n, n_hi - 2)) * p.R + k0;
+    auto load_b = [&](int g, int n) {
+        const uint16_t *base = static_cast<const uint16_t *>(p.lora_b) + ((long)g * p.N + min(n, n_hi - 2)) * p.R;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                b[c][h] = k0 + 8 * h < p.R ? __ldg(reinterpret_cast<const uint4 *>(base + (long)c * p.R) + h)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+                b[c][h] = 8 * h < p.R ? __ldg(reinterpret_cast<const uint4 *>(base + (long)c * p.R) + h)
+                                      : make_uint4(0u, 0u, 0u, 0u);
     };
     uint32_t cv[SB];
     auto load_c = [&](int s0, int s1, int n) {
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
     auto load_job = [&]() {
         const int g = u.adapter[seg];
         if (g >= 0) {
-            load_b(g, n0 + 2 * lane, 0);
+            load_b(g, n0 + 2 * lane);
             load_c(u.first[seg], u.first[seg + 1], n0 + 2 * lane);
         }
     };
@@ -337,38 +336,34 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
 #pragma unroll
         for (int s = 0; s < SB; ++s)
             acc[s][0] = acc[s][1] = 0.0f;
-        for (int k0 = 0; k0 < p.R; k0 += 16) {
-            if (k0 > 0)
-                load_b(g, n, k0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float w[2][8];
+        for (int h = 0; h < 2; ++h) {
+            float w[2][8];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t raw[4] = {b[c][h].x, b[c][h].y, b[c][h].z, b[c][h].w};
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t raw[4] = {b[c][h].x, b[c][h].y, b[c][h].z, b[c][h].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = unpack2<BF16>(raw[i]);
-                        w[c][2 * i] = f.x;
-                        w[c][2 * i + 1] = f.y;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<BF16>(raw[i]);
+                    w[c][2 * i] = f.x;
+                    w[c][2 * i + 1] = f.y;
                 }
-                if (k0 + 8 * h >= p.R) // past R: neither v nor B
-                    break;
+            }
+            if (8 * h >= p.R) // past R: neither v nor B
+                break;
 #pragma unroll
-                for (int s = 0; s < SB; ++s) {
-                    if (s < s0 || s >= s1)
-                        continue;
+            for (int s = 0; s < SB; ++s) {
+                if (s < s0 || s >= s1)
+                    continue;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 v = part[s * r4 + (k0 + 8 * h) / 4 + i];
+                for (int i = 0; i < 2; ++i) {
+                    const float4 v = part[s * r4 + 2 * h + i];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            acc[s][c] = fmaf(v.x, w[c][4 * i], acc[s][c]);
-                            acc[s][c] = fmaf(v.y, w[c][4 * i + 1], acc[s][c]);
-                            acc[s][c] = fmaf(v.z, w[c][4 * i + 2], acc[s][c]);
-                            acc[s][c] = fmaf(v.w, w[c][4 * i + 3], acc[s][c]);
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        acc[s][c] = fmaf(v.x, w[c][4 * i], acc[s][c]);
+                        acc[s][c] = fmaf(v.y, w[c][4 * i + 1], acc[s][c]);
+                        acc[s][c] = fmaf(v.z, w[c][4 * i + 2], acc[s][c]);
+                        acc[s][c] = fmaf(v.w, w[c][4 * i + 3], acc[s][c]);
                     }
                 }
             }

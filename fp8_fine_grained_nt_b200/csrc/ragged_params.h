@@ -17,7 +17,7 @@ enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 =
 // for 32768 rows; swapped: 159 -> 146 us for 128 rows over 16 groups).  128 x 128
 // tiles are used for sums so short that a stage of 64 is enough (45 against 50
 // us for about 31 rows per group).
-__host__ __device__ constexpr int ragged_halves(bool swap, bool pair, int bn)
+__host__ __device__ constexpr int ragged_halves(bool swap, bool pair)
 {
     return pair || swap ? 2 : 1;
 }
