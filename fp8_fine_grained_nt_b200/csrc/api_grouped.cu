@@ -41,25 +41,27 @@ constexpr int kMaxSlots = 1 << 30; // rows and slots are counted in 32 bits, wit
 // twice the mean.  Back to back, these calls run under the power limit (1.2 to
 // 1.7 GHz), so the products that a form issues for padding rows cost time even
 // where memory bounds the call.  The constants were fitted to calls measured
-// that way on B200 (2 to 256 rows per group in 8 to 64 groups for NT and NN,
-// every form; the form taken is 1 % slower than the best on average, 10 % at
-// most) and, for TN, to 18 calls of 16 to 1024 rows per group (1 %, 8 %).
-// Some of them, us (SWAP by BN):
+// that way on B200, every form.  Over 20 calls of NT and NN of 2 to 256 rows per
+// group in 1 to 64 groups, the form taken is 2 % slower than the best one on
+// average, 13 % at most; where all groups have the same count, which the model
+// does not expect, 7 % and 27 % (NN, 8 groups of 128 rows: pairs 57 us, BN = 128
+// 45).  TN, 36 calls of 16 to 1024 rows: 1 % and 12 %; same counts 3 % and 24 %.
+// Some of them, us, counts spread (SWAP by BN; * the form taken):
 //                                           16   32   64  128  128x256  pair
-//   NT 16 groups, N=4096, K=7168,  8 rows  146  152  158  170      161   209
-//                                 64 rows  442  258  213  192      179   237
-//                                256 rows             499  388      331   347
-//   NN  8 groups, N=7168, K=2048, 16 rows   58   36   38   44       51    55
-//                                128 rows       109   90   78       65    67
-//   NN 64 groups, N=2112, K=2048, 16 rows  104   87   92  108      102   137
-// and of BN = 16 shared by 1, 2, 4 and 8 CTAs:
-//   NT  1 group,  N=256,  K=7168, 10 rows   29   19   13    9
-//   NT 16 groups, N=4096, K=7168,  8 rows  145  144  144  171
-//   NT 64 groups, N=2112, K=2048,  8 rows   86  100  136  228
+//   NT 16 groups, N=4096, K=7168,  8 rows  139* 145  150  158      151   198
+//                                 64 rows  445  240  190  167     169*   241
+//                                256 rows            410  324     320*   319
+//   NN  8 groups, N=7168, K=2048, 16 rows   58   40*  38   40       56    53
+//                                128 rows       109   85   71       64    59*
+//   NN 64 groups, N=2112, K=2048, 16 rows  102   90*  85   94       97   126
+// and of BN = 16 shared by 1, 2, 4 and 8 CTAs (all groups alike):
+//   NT  1 group,  N=256,  K=7168, 10 rows   30   19   13    9*
+//   NT 16 groups, N=4096, K=7168,  8 rows  151* 150  145  159
+//   NT 64 groups, N=2112, K=2048,  8 rows   89* 100  112  198
 //                                          128x128  128x256  pair
-//   TN 64 groups, N=2048, K=520, 64 rows        43       46    48
-//                              1024 rows       259      229   190
-//   TN  8 groups, N=7168, K=2048, 16 rows       53       46    49
+//   TN 64 groups, N=2048, K=520, 64 rows       46*       46    51
+//                              1024 rows       303      244  211*
+//   TN  8 groups, N=7168, K=2048, 16 rows       59      48*    49
 double ragged_estimate(const RaggedKernel &k, int split, int groups, int rows, int N, int K, int sms)
 {
     const double cycles_per_us = 1900.0;
@@ -220,7 +222,7 @@ int run_ragged(int dir, const void *A, const void *B, void *D, const int *offset
     // shared memory: the deepest operand ring beside the output staging
     const uint32_t stage = (uint32_t)halves * (128u * 128u + y_rows * 128u);
     // (one slot per epilogue warp beside the wide tiles: the stage it leaves room
-    // for is worth more, 149 -> 142 us for 128 rows over 16 groups)
+    // for is worth more, 1728 -> 1491 us for 32768 rows over 8 groups by pairs)
     const int slots = k->swap ? 0 : k->bn == 256 ? 1 : 2;
     int stages = RAGGED_MAX_STAGES;
     for (; stages >= 2; --stages) {

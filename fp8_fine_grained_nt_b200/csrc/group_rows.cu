@@ -4,8 +4,9 @@
 //   offsets[g + 1] = offsets[g] + ceil(rows of g / alignment) * alignment
 //   slot(r) = offsets[g] + number of rows r' < r with the same group g
 //
-// Bound by latency: 4.7 us a call for 512 rows, 8.0 us for 262144 rows of 64
-// groups, whose arrays (5 MB) are read and written in 0.8.  A short call is
+// Bound by latency: 5.0 us a call for 512 rows, 8.0 us for 262144 rows of 64
+// groups, whose arrays (5 MB) are read and written in 0.8 (of 512 groups 15 us, of
+// 1024 46: every CTA adds up the counts of all chunks).  A short call is
 // done by one CTA in one launch.  Beyond that the rows are cut into contiguous
 // chunks: one kernel counts each chunk's rows per group, a second one adds up
 // the counts of the chunks before its own and places its rows.  No atomics on

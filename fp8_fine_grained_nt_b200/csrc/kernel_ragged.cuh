@@ -15,9 +15,8 @@
 // zero, a bias that grows with the length: nothing beside the rounding to 16
 // bits, but 4e-6 of an FP32 weight gradient over 2048 rows (and 3e-5 over
 // 16384).  So FP32 results (direction TN32) are added up in registers, rounded
-// to nearest, from partial sums of 512 rows: 5e-7, for 7 % of the time (477 ->
-// 510 us at 16384 rows, N = 7168, K = 2048, with stages of 64 rows; partial
-// sums of 256 rows cost 15 %).
+// to nearest, from partial sums of 512 rows: 5e-7, for 4 % of the time (452 ->
+// 469 us back to back at 16384 rows of 8 groups, N = 7168, K = 2048).
 //
 // Tile forms:
 //   PAIR   256 x 256 by a cluster of two CTAs (cta_group::2): each CTA loads
@@ -34,12 +33,17 @@
 //          rows) through distributed shared memory, and adds up what it
 //          receives in rank order.
 //
-// Long groups are bound by the tensor core: 8192 x 8192 x 8192 takes 711 us,
-// 1546 TFLOP/s (a library product of that size: 1613); back to back the power
-// limit holds both near 1370.  Few rows per group are bound by reading the
-// weights: 128 rows over 16 groups, N = 4096, K = 7168, 155 us, 6.1 TB/s.
-// Weight gradients of short groups are bound by writing the result: 1999 rows
-// over 64 groups, 2048 x 520 into BF16, 44 us (a plain fill of those 136 MB: 36).
+// Long groups are bound by the tensor core: 8192 x 8192 x 8192 takes 686 us
+// alone, 1603 TFLOP/s (a library product of that size: 650 us); back to back,
+// under the power limit, 812 us (776).  Few rows per group are bound by reading
+// the weights: 128 rows over 16 groups, N = 4096, K = 7168, 152 us, 6.2 TB/s.
+// Weight gradients of short groups are bound by writing the result as far as
+// its rows are whole 32-byte sectors and its columns fill the tiles: 1999 rows
+// over 64 groups, 2048 x 512 into BF16, 33 us for 134 MB (a plain fill of them
+// takes 36).  528 columns take 39 us, for a fifth tile of 128, as do 576 (640: 40);
+// 520 take 44, where every other row begins and ends in half a sector.
+// Tiles go to the CTAs in turn, whatever their groups' lengths: in the case of
+// 16384 rows above the busiest pair has 8 % more rows than the mean.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
@@ -82,7 +86,7 @@ struct RaggedTile {
     int rows;  // rows of the segment
     int i0;    // tile's first X row: token (relative to the segment) or output index
     int j0;    // tile's first Y row
-    int nkb;   // 64-wide blocks of the reduction
+    int nkb;   // blocks (stages, BK wide) of the reduction
 };
 
 __device__ __forceinline__ int fast_div(int n, const FastDiv &f)
@@ -93,8 +97,7 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv &f)
 // Tile t.  `tiles` holds the tile prefix sums of the groups (NT, NN); `g` is
 // the group of the caller's previous (lower) tile.  Order within a group: bands
 // of 8 X blocks, X fastest within a band, so that the tiles in flight share
-// both operands in L2 (measured at 8192 x 8192 x 8192: bands of 8 741 us, of 4
-// 756 us, of 16 754 us).  SWAP: the token blocks of one weight block run side
+// both operands in L2 (8192 x 8192 x 8192: bands of 4 and of 16 were 2 % slower).  SWAP: the token blocks of one weight block run side
 // by side.
 template <int DIR, bool SWAP, int BM, int BN, int BK>
 __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, int &g, const int *tiles,

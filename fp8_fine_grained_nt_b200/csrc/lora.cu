@@ -10,7 +10,8 @@
 // Both factors are thin, so neither bytes (1.5 us for 64 rows of 28 adapters,
 // rank 16, K = 2048, N = 7168) nor products bound the operator but the latency
 // of its chain: slots, loads, sums, v out and in again, loads, stores.  It
-// takes 10.5 us there and 6.6 us for one row.  So the work is cut into about
+// takes 8.4 us a call there and 6 for one row (replayed from a graph, as all
+// times in this file; 64 rows in no order, with an index, 10.2).  So the work is cut into about
 // four CTAs per SM, every load is issued as early as its address is known, and
 // the products run on operands loaded straight from global memory into
 // registers (a 16-byte load gives a lane of the first kernel 8 consecutive
@@ -38,8 +39,9 @@ constexpr int LORA_THREADS = 256;
 constexpr int LORA_WARPS = 8;
 constexpr int LORA_SLOTS = 16;   // slots per CTA of the first kernel: one MMA's rows
 constexpr int LORA_UP_SLOTS = 8; // of the second
-// Largest rank whose second product is done in FP32 (64 rows of 28 adapters: rank
-// 16 11.3 us, with mma.sync 13.3; rank 32 17.4 and 14.4).
+// Largest rank whose second product is done in FP32 (64 rows of 28 adapters, N =
+// 7168, K = 2048: rank 8 7.7 us, with mma.sync 9.7; rank 16 8.4 and 9.5; rank 32
+// 12.8 and 10.5).
 constexpr int LORA_FP32_RANK = 16;
 
 // bytes of v's sums, or of their shares
@@ -259,8 +261,7 @@ __device__ __forceinline__ void sum_ranges(const LoraParams &p, int slot0, float
 // Ranks up to 16: 8 slots and `p.n_chunk` columns per CTA.  A warp's job is 64 columns of one
 // segment, two per lane, all ranks in FP32: with one or two rows per
 // adapter, as in a decode batch, that takes a third of the instructions of an
-// MMA with its 16 rows (alone, with cold caches, 13.5 -> 8.8 us for 64 rows of
-// 28 adapters, N = 7168).
+// MMA with its 16 rows.
 template <bool BF16>
 __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraParams p)
 {
@@ -386,10 +387,11 @@ __global__ void __launch_bounds__(LORA_THREADS, 4) lora_up_kernel(const LoraPara
 // with mma.sync, v in two 16-bit terms (hi + lo: 16 bits of mantissa with BF16,
 // 22 with FP16, so that the middle result costs no accuracy; an FP16 row is
 // divided by a power of two first, so that v may exceed its range).  Rank 64,
-// 64 rows of 28 adapters, N = 7168, K = 2048: FP32 took 25.6 us a call, most of it reading
-// B, whose columns a lane of that form has 2 R bytes from the next lane's; here
-// four lanes read 64 bytes of a column: 21.5 us (256 rows: 41.5 -> 27.6; rank
-// 32: 17.4 -> 14.4).  The MMA's columns are dealt out so that a lane's results
+// 64 rows of 28 adapters, N = 7168, K = 2048: in FP32 20.2 us a call, most of it
+// reading B, whose columns a lane of that form has 2 R bytes from the next lane's;
+// here four lanes read 64 bytes of a column: 15.9 us, where the weights take 5
+// (256 rows: 38.1 -> 22.3).  Half of an MMA's rows are empty, and adapters that
+// begin within 8 slots are read by both their blocks.  The MMA's columns are dealt out so that a lane's results
 // are 8 columns side by side.
 template <bool BF16>
 __global__ void __launch_bounds__(LORA_THREADS, 3) lora_up_mma_kernel(const LoraParams p)
@@ -592,7 +594,7 @@ void set_columns(LoraParams &p, long chunks)
 
 // How a call is cut up, from its sizes alone (the workspace follows from it):
 // k ranges and column chunks so that either kernel has about four CTAs per SM
-// (three with mma.sync in the second: rank 64, 64 rows 21.5 us, 24.6 with four),
+// (three with mma.sync in the second: rank 64, 64 rows 15.9 us, 17.1 with four),
 // at most 32 ranges (which the second kernel adds up in one or two rounds of
 // loads), at least 64 wide.
 void lora_plan(LoraParams &p)

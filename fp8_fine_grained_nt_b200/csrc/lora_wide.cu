@@ -700,13 +700,20 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const WideParam
 } // namespace
 
 // Long batches with enough slots per adapter; grid.y counts blocks of slots.
-// Measured, short form against this one, us (N = 4096, K = 7168, rank 64):
-//                     256 rows   512       768       1024      2048
-//   1 adapter         17, 24     21, 24    28, 24    32, 24    55, 35
-//   8 adapters        20, 50     26, 33    32, 31    38, 31    68, 52
-//   8 of rank 16      12, 43     18, 27    22, 26    28, 26    48, 41
-//   32 rows of each   20, 50     28, 51    40, 52    47, 53    102, 88
-// (with fewer rows of each, a block of slots makes more passes)
+// Measured, short form against this one, us from graphs (N = 4096, K = 7168, rank
+// 64 but where said):
+//                     256 rows   512      768      1024     2048     4096
+//   1 adapter         16, 23     20, 23   26, 23   29, 24   51, 34    99, 36
+//   8 adapters        16, 31     20, 23   26, 23   29, 24   52, 34   102, 37
+//   8 of rank 16       9, 25     14, 22   16, 22   19, 22   31, 32    60, 35
+//   2 of rank 128     20, 28     27, 28   36, 29   43, 29   84, 42   162, 45
+//   32 rows of each   16, 31     20, 31   26, 31   32, 32   60, 53   111, 65
+// One limit for all of them: it loses up to a fifth between 513 and 768 slots at
+// ranks above 64 and between 769 and 2000 at rank 16.
+// The host knows the adapters loaded, not those in use: an unsorted batch of many
+// would make up to 32 passes (128 above rank 64) over each block of slots.  So a
+// few adapters of a large pool take the short form too: 4096 rows of 8 adapters
+// 38 us with up to 128 loaded, 101 with more (of 129 in use 155, of 128 65).
 bool lora_is_wide(int slots, int adapters, int R)
 {
     return slots > 768 && R <= 128 && slots / adapters >= 32 && slots <= 65535 * WIDE_SLOTS;

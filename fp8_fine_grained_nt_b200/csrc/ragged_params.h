@@ -13,10 +13,9 @@ enum RaggedOut : int { RAGGED_OUT_F32 = 0, RAGGED_OUT_BF16 = 1, RAGGED_OUT_F16 =
 
 // 64-wide blocks of the reduction (128-byte swizzled rows) per stage.  Two where
 // three such stages fit: the thread that issues the MMAs then waits and commits
-// half as often, and it is what holds these kernels back (pairs: 1405 -> 1320 us
-// for 32768 rows; swapped: 159 -> 146 us for 128 rows over 16 groups).  128 x 128
-// tiles are used for sums so short that a stage of 64 is enough (45 against 50
-// us for about 31 rows per group).
+// half as often, and it is what holds these kernels back (N = 4096, K = 7168, pairs:
+// 1590 -> 1491 us back to back for 32768 rows over 8 groups; swapped: 157 -> 152 us
+// for 128 rows over 16).
 __host__ __device__ constexpr int ragged_halves(bool swap, bool pair)
 {
     return pair || swap ? 2 : 1;
@@ -59,7 +58,7 @@ struct RaggedParams {
     int total_rows;      // rows of the token tensors
     int d_rows;          // TN: rows of one group's result (N)
     int d_cols;          // columns of the result
-    int nkb;             // NT, NN: 64-wide blocks of the reduction
+    int nkb;             // NT, NN: blocks (64 * ragged_halves wide) of the reduction
     int x_blocks;        // SWAP: blocks of 128 output columns; TN: blocks of X rows
     int y_blocks;        // NT, NN without SWAP: blocks of output columns; TN: blocks of Y rows
     FastDiv tiles_per_group; // TN

@@ -151,8 +151,10 @@ int quantize_fp8_1x128(const void *x, int x_dtype, void *q, float *sa, int M, in
  *            the end of the segment before it.
  * Everything row-major and dense; N % 8 == 0, K % 8 == 0 (16-byte rows),
  * 1 <= num_groups <= 1024; M_sum, N and K <= 0x7fff0000.  Sums are FP32 over the
- * whole reduction, rounded once (to nearest even) to D's type.  D must not overlap
- * A or B. */
+ * whole reduction, rounded once (to nearest even) to D's type.  The tensor core
+ * adds 16 products at a time and truncates (about 2e-9 of the sum per element of
+ * the reduction, towards zero); FP32 results are joined from partial sums of 512
+ * rows, which keeps them within 1e-6.  D must not overlap A or B. */
 
 /* Forward: D[t,n] = sum_k A[t,k] * B[g,n,k] for t in segment g.
  *   A [M_sum,K]   B [num_groups,N,K]   D [M_sum,N] */
@@ -215,7 +217,8 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups);
  * and row t = order[i] (t = i if order is NULL):
  *   D[t,n] = C[t,n] + scales[g] * sum_r ( sum_k X[t,k] A[g,r,k] ) B[g,n,r]
  * with FP32 sums throughout (the inner sums keep at least 16 bits of mantissa:
- * FP32, or two 16-bit terms) and one rounding to D's type (to nearest even).
+ * FP32, or two 16-bit terms, with which an infinite element of B may give NaN for
+ * an infinity) and one rounding to D's type (to nearest even).
  *   X [num_rows] rows of K   A [num_adapters,rank,K]   C, D [num_rows] rows of N
  *   B [num_adapters,N,rank]  scales [num_adapters] FP32
  * all but scales of type dtype (DG_INPUT_BF16 or DG_INPUT_F16).  ld_x, ld_c,
@@ -229,7 +232,10 @@ long long get_group_rows_workspace_size(int num_rows, int num_groups);
  *             group_rows_by_index orders them) share the reads of its weights.
  * A value out of range sets DG_ERR_DEVICE_BAD_INDEX and its slot is skipped.
  * rank: a multiple of 8, at most 256 (smaller adapters: zero rows of A and
- * columns of B); N % 8 == 0, K % 8 == 0, both <= 0x7fff0000.  workspace: at least
+ * columns of B); N % 8 == 0, K % 8 == 0, both <= 0x7fff0000.  Above 768 slots, up
+ * to rank 128 and with at least 32 slots per adapter of num_adapters (those loaded:
+ * which are in use is known on the device only), one kernel computes blocks of 128
+ * slots; other long batches take up to 3.5 times as long.  workspace: at least
  * get_lora_workspace_size(num_slots, num_adapters, rank, N, K) bytes (0 for
  * long batches), 16-byte aligned, in use until the call's work has completed;
  * calls that may run at the same time need one each. */
