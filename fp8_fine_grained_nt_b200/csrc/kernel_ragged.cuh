@@ -41,15 +41,16 @@
 // its rows are whole 32-byte sectors and its columns fill the tiles: 1999 rows
 // over 64 groups, 2048 x 512 into BF16, 33 us for 134 MB (a plain fill of them
 // takes 36).  528 columns take 39 us, for a fifth tile of 128, as do 576 (640: 40);
-// 520 take 44, where every other row begins and ends in half a sector.
+// 520 take 44: every other boundary between rows lies within a sector.
 // Tiles go to the CTAs in turn, whatever their groups' lengths: in the case of
 // 16384 rows above the busiest pair has 8 % more rows than the mean.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 TMEM
 // allocator and MMA issuer, warp 2 clears the rows behind a segment's end (TN
-// only), warp 3 hands back received sums (shared reductions), warps 4-11 epilogue (a 32-lane quarter of tensor memory and half of the
-// tile's columns each).  Two accumulators in tensor memory let a tile's
-// epilogue overlap the next tile's MMAs.
+// only), warp 3 hands back received sums (shared reductions), warps 4-11
+// epilogue (a 32-lane quarter of tensor memory and half of the tile's columns
+// each).  Two accumulators in tensor memory let a tile's epilogue overlap the
+// next tile's MMAs.
 #pragma once
 
 #include "kernel.cuh"
@@ -97,8 +98,8 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv &f)
 // Tile t.  `tiles` holds the tile prefix sums of the groups (NT, NN); `g` is
 // the group of the caller's previous (lower) tile.  Order within a group: bands
 // of 8 X blocks, X fastest within a band, so that the tiles in flight share
-// both operands in L2 (8192 x 8192 x 8192: bands of 4 and of 16 were 2 % slower).  SWAP: the token blocks of one weight block run side
-// by side.
+// both operands in L2 (8192 x 8192 x 8192: bands of 4 and of 16 were 2 % slower).
+// SWAP: the token blocks of one weight block run side by side.
 template <int DIR, bool SWAP, int BM, int BN, int BK>
 __device__ __forceinline__ RaggedTile ragged_tile(const RaggedParams &p, int t, int &g, const int *tiles,
                                                   const int *first, const int *count)

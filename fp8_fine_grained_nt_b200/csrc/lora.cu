@@ -11,13 +11,13 @@
 // rank 16, K = 2048, N = 7168) nor products bound the operator but the latency
 // of its chain: slots, loads, sums, v out and in again, loads, stores.  It
 // takes 8.4 us a call there and 6 for one row (replayed from a graph, as all
-// times in this file; 64 rows in no order, with an index, 10.2).  So the work is cut into about
-// four CTAs per SM, every load is issued as early as its address is known, and
-// the products run on operands loaded straight from global memory into
-// registers (a 16-byte load gives a lane of the first kernel 8 consecutive
-// elements of the reduction, which any pairing of mma.sync's k positions may
-// use as long as both operands use the same one).  Two kernels, the second set
-// up while the first runs:
+// times in this file; 64 rows given by an index, of 32 adapters or none, 10.2).
+// So the work is cut into about four CTAs per SM, every load is issued as early
+// as its address is known, and the products run on operands loaded straight
+// from global memory into registers (a 16-byte load gives a lane of the first
+// kernel 8 consecutive elements of the reduction, which any pairing of
+// mma.sync's k positions may use as long as both operands use the same one).
+// Two kernels, the second set up while the first runs:
 //   down  v in FP32 for a range of k per CTA (`splits` ranges, written side by
 //         side: summed in order by the second kernel, so no atomics)
 //   up    sums the ranges and adds v B^T to c, rounding once.

@@ -261,11 +261,13 @@ int get_tma_aligned_size(int x, int element_size);
 
 /* Upper bound on the SMs the kernels use (DeepGEMM README, utility
  * functions: set_num_sms / get_num_sms): no launch of the GEMMs, the ragged
- * products, the grouping and the adapters has more CTAs than that (the
- * quantiser's are not bounded).  Workspace sizes do not depend on it; the
- * adapters' sums may be cut differently, and so differ in their last bits.  n <= 0 restores "all SMs of the current device".
- * Returns DG_OK.  get_num_sms() returns the bound in force
- * (the device's SM count when unset and a device is present, else 0). */
+ * products, the grouping and the adapters has more CTAs than that, except that a
+ * dense call of M <= 256 may take one cluster of up to 8; the quantiser's are not
+ * bounded.  Workspace sizes do not depend on it; the adapters' sums may be cut
+ * differently, and so differ in their last bits.
+ * n <= 0 restores "all SMs of the current device".  Returns DG_OK.
+ * get_num_sms() returns the bound in force (the device's SM count when unset
+ * and a device is present, else 0). */
 int set_num_sms(int n);
 int get_num_sms(void);
 
